@@ -2,7 +2,8 @@
 
 The layer runs in ``libmoe_gb300.so`` (hand-written CUDA for sm_103a behind the C ABI of
 ``include/moe.h``). This package is the Python binding (``_lib``, same function names as
-the C ABI) plus ``layer.MoELayer``, which owns the workspace and calls ``moe_forward``.
+the C ABI), ``layer.MoELayer``, which owns the workspace and calls ``moe_forward``, and
+``training``, the operators of a training step (``include/moe_train.h``) on tensors.
 """
 from ._lib import (EXPORTED, MOE_BF16, MOE_F32, MOE_GEMM_DECODE_TC,  # noqa: F401
                    MOE_GEMM_INVALID, MOE_GEMM_PAIR_TC, MOE_GEMM_SIMT, MOE_GEMM_SMALL_BATCH,
@@ -19,3 +20,10 @@ from ._lib import (EXPORTED, MOE_BF16, MOE_F32, MOE_GEMM_DECODE_TC,  # noqa: F40
                    moe_masked_table, moe_masked_workspace_size, moe_max_padded_rows, moe_route,
                    moe_small_batch, moe_route_logits, moe_selftest_wait_timeout,
                    moe_workspace_layout, moe_workspace_size, status_string)
+from ._lib import (MOE_GATE_CHANNEL, MOE_GATE_FULL, MOE_GATE_NONE, MOE_GATE_TOKEN,  # noqa: F401
+                   MOE_TRAIN_BLOCK, moe_block_join, moe_block_join_backward, moe_block_norm,
+                   moe_block_norm_backward, moe_block_t, moe_block_workspace_size,
+                   moe_expert_down, moe_expert_down_backward, moe_expert_up,
+                   moe_expert_up_backward, moe_expert_weight_grad, moe_experts_t, moe_permute,
+                   moe_permute_backward, moe_route_backward, moe_unpermute,
+                   moe_unpermute_backward)

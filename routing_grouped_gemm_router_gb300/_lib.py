@@ -1,4 +1,5 @@
-"""ctypes binding of libmoe_gb300.so: the C ABI of include/moe.h under the same names.
+"""ctypes binding of libmoe_gb300.so: the C ABI of include/moe.h and moe_train.h under the same
+names.
 
 Argument marshalling only: tensors become device pointers (``data_ptr()``), streams become
 ``cudaStream_t`` handles, and a non-OK status raises ``MoeError``. Every step of the layer
@@ -18,6 +19,8 @@ MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_CUD
 MOE_F32, MOE_BF16 = 0, 1
 MOE_ROUTE_SOFTMAX, MOE_ROUTE_SIGMOID_GROUPED = 0, 1
 MOE_WEIGHTS_NATIVE, MOE_WEIGHTS_FP8_E4M3_B128 = 0, 1
+MOE_TRAIN_BLOCK = 16  # rows an expert's run is padded to in the training operators
+MOE_GATE_NONE, MOE_GATE_CHANNEL, MOE_GATE_TOKEN, MOE_GATE_FULL = range(4)
 
 
 class MoeError(RuntimeError):
@@ -45,6 +48,16 @@ class moe_ws_layout_t(ctypes.Structure):
                [("block_m", ctypes.c_int), ("max_padded", ctypes.c_int)]
 
 
+class moe_experts_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("rows", "E", "H", "I", "dtype")]
+
+
+class moe_block_t(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int), ("H", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("gate_kind", ctypes.c_int), ("scale", ctypes.c_float),
+                ("offset", ctypes.c_float), ("eps", ctypes.c_float)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing: build it with "
@@ -52,6 +65,7 @@ def _load():
     lib = ctypes.CDLL(LIB_PATH)
     P, I32, SZ, ST = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_int
     CFG = ctypes.POINTER(moe_config_t)
+    EXP, BLK = ctypes.POINTER(moe_experts_t), ctypes.POINTER(moe_block_t)
     sig = {
         "moe_abi_version": (I32, []),
         "moe_status_string": (ctypes.c_char_p, [ST]),
@@ -85,6 +99,21 @@ def _load():
         "moe_selftest_wait_timeout": (ST, [P]),
         "moe_route_logits": (ST, [CFG, P, P, P, P]),
         "moe_dequant_fp8_weights": (ST, [CFG, I32, P, P, P, P]),
+        "moe_permute": (ST, [P, P, P, I32, I32, I32, I32, I32, I32, P, P, P]),
+        "moe_permute_backward": (ST, [P, P, I32, I32, I32, I32, I32, P, P]),
+        "moe_unpermute": (ST, [P, P, P, I32, I32, I32, I32, I32, P, P]),
+        "moe_unpermute_backward": (ST, [P, P, P, P, P, I32, I32, I32, I32, I32, P, P, P]),
+        "moe_expert_up": (ST, [EXP, P, P, P, P, P, P]),
+        "moe_expert_down": (ST, [EXP, P, P, P, P, P]),
+        "moe_expert_down_backward": (ST, [EXP, P, P, P, P, P, P, P]),
+        "moe_expert_up_backward": (ST, [EXP, P, P, P, P, P]),
+        "moe_expert_weight_grad": (ST, [I32, I32, I32, I32, I32, I32, I32, P, P, P, P, P]),
+        "moe_block_workspace_size": (ST, [BLK, ctypes.POINTER(SZ)]),
+        "moe_block_norm": (ST, [BLK, P, P, P, P, P]),
+        "moe_block_norm_backward": (ST, [BLK, P, P, P, P, P, P, P, P, SZ, P]),
+        "moe_block_join": (ST, [BLK, P, P, P, P, P, P, P, P, P, P]),
+        "moe_block_join_backward": (ST, [BLK] + [P] * 15 + [SZ, P]),
+        "moe_route_backward": (ST, [CFG, P, P, P, P, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -104,7 +133,12 @@ EXPORTED = ("moe_abi_version", "moe_status_string", "moe_block_m", "moe_small_ba
             "moe_grouped_swiglu", "moe_combine", "moe_apply_expert_map", "moe_combine_local",
             "moe_masked_table", "moe_masked_workspace_size", "moe_masked_forward",
             "moe_forward", "moe_device_status", "moe_selftest_wait_timeout",
-            "moe_route_logits", "moe_dequant_fp8_weights")
+            "moe_route_logits", "moe_dequant_fp8_weights",
+            "moe_permute", "moe_permute_backward", "moe_unpermute", "moe_unpermute_backward",
+            "moe_expert_up", "moe_expert_down", "moe_expert_down_backward",
+            "moe_expert_up_backward", "moe_expert_weight_grad", "moe_block_workspace_size",
+            "moe_block_norm", "moe_block_norm_backward", "moe_block_join",
+            "moe_block_join_backward", "moe_route_backward")
 
 
 def lib():
@@ -342,3 +376,95 @@ def moe_forward(cfg, x, Wg, W13, W2, out, ws, ws_bytes, stream=None):
 
 def moe_device_status(reset=True) -> int:
     return _lib.moe_device_status(int(bool(reset)))
+
+
+# ------------------------------------------------------------------------ training operators
+
+def moe_permute(x, topk_ids, sorted_ids, T, k, E, H, dtype, rows, xs, row_pos, stream=None):
+    _check("moe_permute", _lib.moe_permute(_ptr(x), _ptr(topk_ids), _ptr(sorted_ids), T, k, E, H,
+                                           dtype, rows, _ptr(xs), _ptr(row_pos), _stream(stream)))
+
+
+def moe_permute_backward(dxs, row_pos, T, k, H, dtype, rows, dx, stream=None):
+    _check("moe_permute_backward", _lib.moe_permute_backward(
+        _ptr(dxs), _ptr(row_pos), T, k, H, dtype, rows, _ptr(dx), _stream(stream)))
+
+
+def moe_unpermute(ys, row_pos, topk_w, T, k, H, dtype, rows, out, stream=None):
+    _check("moe_unpermute", _lib.moe_unpermute(_ptr(ys), _ptr(row_pos), _ptr(topk_w), T, k, H,
+                                               dtype, rows, _ptr(out), _stream(stream)))
+
+
+def moe_unpermute_backward(dout, ys, sorted_ids, row_pos, topk_w, T, k, H, dtype, rows, dys,
+                           dtopk_w, stream=None):
+    _check("moe_unpermute_backward", _lib.moe_unpermute_backward(
+        _ptr(dout), _ptr(ys), _ptr(sorted_ids), _ptr(row_pos), _ptr(topk_w), T, k, H, dtype,
+        rows, _ptr(dys), _ptr(dtopk_w), _stream(stream)))
+
+
+def moe_expert_up(cfg, xs, W13, counts, h13, act, stream=None):
+    _check("moe_expert_up", _lib.moe_expert_up(ctypes.byref(cfg), _ptr(xs), _ptr(W13),
+                                               _ptr(counts), _ptr(h13), _ptr(act),
+                                               _stream(stream)))
+
+
+def moe_expert_down(cfg, act, W2, counts, ys, stream=None):
+    _check("moe_expert_down", _lib.moe_expert_down(ctypes.byref(cfg), _ptr(act), _ptr(W2),
+                                                   _ptr(counts), _ptr(ys), _stream(stream)))
+
+
+def moe_expert_down_backward(cfg, dys, W2, h13, counts, dh13, act, stream=None):
+    _check("moe_expert_down_backward", _lib.moe_expert_down_backward(
+        ctypes.byref(cfg), _ptr(dys), _ptr(W2), _ptr(h13), _ptr(counts), _ptr(dh13), _ptr(act),
+        _stream(stream)))
+
+
+def moe_expert_up_backward(cfg, dh13, W13, counts, dxs, stream=None):
+    _check("moe_expert_up_backward", _lib.moe_expert_up_backward(
+        ctypes.byref(cfg), _ptr(dh13), _ptr(W13), _ptr(counts), _ptr(dxs), _stream(stream)))
+
+
+def moe_expert_weight_grad(rows, E, M, N, dtype, out_dtype, accumulate, dy, a, counts, dW,
+                           stream=None):
+    _check("moe_expert_weight_grad", _lib.moe_expert_weight_grad(
+        rows, E, M, N, dtype, out_dtype, int(bool(accumulate)), _ptr(dy), _ptr(a), _ptr(counts),
+        _ptr(dW), _stream(stream)))
+
+
+def moe_block_workspace_size(cfg) -> int:
+    out = ctypes.c_size_t(0)
+    _check("moe_block_workspace_size",
+           _lib.moe_block_workspace_size(ctypes.byref(cfg), ctypes.byref(out)))
+    return out.value
+
+
+def moe_block_norm(cfg, x, gamma, h, rstd, stream=None):
+    _check("moe_block_norm", _lib.moe_block_norm(ctypes.byref(cfg), _ptr(x), _ptr(gamma), _ptr(h),
+                                                 _ptr(rstd), _stream(stream)))
+
+
+def moe_block_norm_backward(cfg, dh, x, gamma, rstd, dres, dx, dgamma, ws, ws_bytes,
+                            stream=None):
+    _check("moe_block_norm_backward", _lib.moe_block_norm_backward(
+        ctypes.byref(cfg), _ptr(dh), _ptr(x), _ptr(gamma), _ptr(rstd), _ptr(dres), _ptr(dx),
+        _ptr(dgamma), _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def moe_block_join(cfg, x, y, gamma, gate, gamma_next, out, rstd_y, h, rstd_out, stream=None):
+    _check("moe_block_join", _lib.moe_block_join(
+        ctypes.byref(cfg), _ptr(x), _ptr(y), _ptr(gamma), _ptr(gate), _ptr(gamma_next),
+        _ptr(out), _ptr(rstd_y), _ptr(h), _ptr(rstd_out), _stream(stream)))
+
+
+def moe_block_join_backward(cfg, dres, dh, out, y, gamma, gate, gamma_next, rstd_y, rstd_out, dx,
+                            dy, dgamma, dgamma_next, dgate, ws, ws_bytes, stream=None):
+    _check("moe_block_join_backward", _lib.moe_block_join_backward(
+        ctypes.byref(cfg), _ptr(dres), _ptr(dh), _ptr(out), _ptr(y), _ptr(gamma), _ptr(gate),
+        _ptr(gamma_next), _ptr(rstd_y), _ptr(rstd_out), _ptr(dx), _ptr(dy), _ptr(dgamma),
+        _ptr(dgamma_next), _ptr(dgate), _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def moe_route_backward(cfg, logits, topk_ids, dtopk_w, dlogits, stream=None):
+    _check("moe_route_backward", _lib.moe_route_backward(
+        ctypes.byref(cfg), _ptr(logits), _ptr(topk_ids), _ptr(dtopk_w), _ptr(dlogits),
+        _stream(stream)))

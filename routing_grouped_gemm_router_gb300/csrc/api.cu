@@ -4,6 +4,7 @@
 #include <mutex>
 
 #include "common.cuh"
+#include "train.cuh"
 
 namespace moe {
 
@@ -653,7 +654,8 @@ int moe_device_status(int reset) {
   const int c = combine_status_read(reset);
   const int t = tiny_status_read(reset);
   const int d = dec_status_read(reset);
-  return g ? g : (d ? d : (r ? r : (a ? a : (t ? t : c))));
+  const int e = train_status_read(reset);
+  return g ? g : (d ? d : (r ? r : (a ? a : (t ? t : (c ? c : e)))));
 }
 
 }  // extern "C"

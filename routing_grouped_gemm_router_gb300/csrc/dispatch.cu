@@ -1,0 +1,222 @@
+// dispatch.cu — token rows sorted by expert and back, with the router weights, and the
+// gradients of both (moe_permute, moe_unpermute and their backward calls).
+//
+// With pos[t, j] the row of slot j of token t in the expert-sorted buffer:
+//   permute             xs[pos[t, j]] = x[t]
+//   its gradient        dx[t] = sum_j dxs[pos[t, j]]
+//   unpermute           out[t] = sum_j w[t, j] ys[pos[t, j]]
+//   its gradients       dys[pos[t, j]] = w[t, j] dout[t],  dw[t, j] = <dout[t], ys[pos[t, j]]>
+// All four move rows and do next to no arithmetic, so HBM bounds them: every row is read and
+// written once, in 16-byte pieces. Sums over slots and over a row are fp32, in a fixed order.
+#include "train.cuh"
+
+namespace moe {
+namespace dispatch {
+
+// ------------------------------------------------------------------- permute
+// One warp a buffer row: the sorted table gives the slot, the slot its token. Reads of a token
+// row by its k copies hit L2. Rows of no slot are written as zeros, so that the expert products
+// may run over whole 16-row steps.
+__global__ void __launch_bounds__(256) permute_kernel(const uint4* __restrict__ x,
+                                                      const int32_t* __restrict__ ids,
+                                                      const int32_t* __restrict__ sid, int n,
+                                                      int k, int E, int rows, int vec,
+                                                      uint4* __restrict__ xs,
+                                                      int32_t* __restrict__ pos) {
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31;
+  // slots without an expert never appear in the table: their position is written here
+  for (int r = blockIdx.x * blockDim.x + threadIdx.x; r < n; r += gridDim.x * blockDim.x) {
+    const int e = ids[r];
+    if (e < 0 || e >= E) pos[r] = -1;
+  }
+  const int warps = gridDim.x * (blockDim.x >> 5);
+  for (int p = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); p < rows; p += warps) {
+    const int r = sid[p];
+    uint4* dst = xs + (int64_t)p * vec;
+    if (r < 0 || r >= n) {
+      const uint4 z = make_uint4(0, 0, 0, 0);
+      for (int v = lane; v < vec; v += 32) dst[v] = z;
+      continue;
+    }
+    if (lane == 0) pos[r] = p;
+    const uint4* src = x + (int64_t)(r / k) * vec;
+    int v = lane;
+    for (; v + 96 < vec; v += 128) {
+      const uint4 a = src[v], b = src[v + 32], c = src[v + 64], d = src[v + 96];
+      dst[v] = a;
+      dst[v + 32] = b;
+      dst[v + 64] = c;
+      dst[v + 96] = d;
+    }
+    for (; v < vec; v += 32) dst[v] = src[v];
+  }
+}
+
+// ------------------------------------------------- sums over a token's slots
+// One thread a 16-byte piece of a token's row; the slots' pieces are loaded four at a time
+// before any is added, so four rows are in flight a thread.
+template <typename T, bool WEIGHTED>
+__global__ void __launch_bounds__(256) slot_sum_kernel(const uint4* __restrict__ ys,
+                                                       const int32_t* __restrict__ pos,
+                                                       const float* __restrict__ w, int k,
+                                                       int rows, int vec, int parts,
+                                                       uint4* __restrict__ out) {
+  pdl_wait();
+  pdl_trigger();
+  const int64_t t = blockIdx.x / parts;
+  const int v = (int)(blockIdx.x % parts) * blockDim.x + threadIdx.x;
+  if (v >= vec) return;
+  constexpr int W = 16 / sizeof(T);
+  float acc[W];
+#pragma unroll
+  for (int i = 0; i < W; ++i) acc[i] = 0.f;
+  for (int j0 = 0; j0 < k; j0 += 4) {
+    uint4 q[4];
+    float wj[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int p = j0 + j < k ? __ldg(pos + t * k + j0 + j) : -1;
+      const bool live = p >= 0 && p < rows;
+      q[j] = live ? __ldcs(ys + (int64_t)p * vec + v) : make_uint4(0, 0, 0, 0);
+      wj[j] = WEIGHTED && live ? __ldg(w + t * k + j0 + j) : (live ? 1.f : 0.f);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float f[W];
+      Vec<T>::unpack(q[j], f);
+#pragma unroll
+      for (int i = 0; i < W; ++i) acc[i] = WEIGHTED ? fmaf(wj[j], f[i], acc[i]) : acc[i] + f[i];
+    }
+  }
+  out[t * vec + v] = Vec<T>::pack(acc);
+}
+
+// ------------------------------------------------- gradients of the weighted sum
+// Blocks 0..T-1: one a token. Its dout row is read once and stays in registers (up to kKeep
+// pieces a thread; longer rows come from L2 again) while the k rows of ys stream past; the dot
+// products of all slots meet in shared memory once, at the end. The blocks after them write
+// zeros into rows of no slot.
+constexpr int kUbThreads = 256;
+constexpr int kKeep = 4;
+constexpr int kZeroRows = 64;  // table entries a zeroing block looks at
+
+template <typename T>
+__global__ void __launch_bounds__(kUbThreads) unpermute_backward_kernel(
+    const uint4* __restrict__ dout, const uint4* __restrict__ ys, const int32_t* __restrict__ sid,
+    const int32_t* __restrict__ pos, const float* __restrict__ w, int Tn, int k, int rows,
+    int vec, uint4* __restrict__ dys, float* __restrict__ dw) {
+  pdl_wait();
+  pdl_trigger();
+  constexpr int W = 16 / sizeof(T);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if ((int)blockIdx.x >= Tn) {
+    const int p0 = ((int)blockIdx.x - Tn) * kZeroRows;
+    const uint4 z = make_uint4(0, 0, 0, 0);
+    for (int p = p0 + warp; p < min(p0 + kZeroRows, rows); p += kUbThreads / 32) {
+      const int r = sid[p];
+      if (r >= 0 && r < Tn * k) continue;
+      for (int v = lane; v < vec; v += 32) dys[(int64_t)p * vec + v] = z;
+    }
+    return;
+  }
+  __shared__ float dots[32][kUbThreads / 32];
+  const int64_t t = blockIdx.x;
+  const uint4* drow = dout + t * vec;
+  uint4 keep[kKeep];
+#pragma unroll
+  for (int i = 0; i < kKeep; ++i) {
+    const int v = threadIdx.x + i * kUbThreads;
+    if (v < vec) keep[i] = drow[v];
+  }
+  for (int j = 0; j < k; ++j) {
+    const int p = __ldg(pos + t * k + j);
+    const bool live = p >= 0 && p < rows;
+    float dot = 0.f;
+    if (live) {
+      const float wj = __ldg(w + t * k + j);
+      const uint4* yrow = ys + (int64_t)p * vec;
+      uint4* orow = dys + (int64_t)p * vec;
+      auto piece = [&](const uint4& dq, const uint4& yq, int v) {
+        float d[W], y[W];
+        Vec<T>::unpack(dq, d);
+        Vec<T>::unpack(yq, y);
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+          dot = fmaf(d[i], y[i], dot);
+          d[i] *= wj;
+        }
+        orow[v] = Vec<T>::pack(d);
+      };
+      uint4 yq[kKeep];
+#pragma unroll
+      for (int i = 0; i < kKeep; ++i) {
+        const int v = threadIdx.x + i * kUbThreads;
+        if (v < vec) yq[i] = __ldcs(yrow + v);
+      }
+#pragma unroll
+      for (int i = 0; i < kKeep; ++i) {
+        const int v = threadIdx.x + i * kUbThreads;
+        if (v < vec) piece(keep[i], yq[i], v);
+      }
+      for (int v = threadIdx.x + kKeep * kUbThreads; v < vec; v += kUbThreads)
+        piece(drow[v], __ldcs(yrow + v), v);
+    }
+    dot = warp_total(dot);
+    if (lane == 0) dots[j][warp] = dot;
+  }
+  __syncthreads();
+  if (threadIdx.x < k) {
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < kUbThreads / 32; ++i) s += dots[threadIdx.x][i];
+    dw[t * k + threadIdx.x] = s;
+  }
+}
+
+}  // namespace dispatch
+
+using namespace dispatch;
+
+moe_status_t launch_permute(const void* x, const int32_t* ids, const int32_t* sid, int T, int k,
+                            int E, int H, moe_dtype_t dt, int rows, void* xs, int32_t* pos,
+                            cudaStream_t s) {
+  const int vec = H * (int)dtype_size(dt) / 16;
+  const int blocks = std::min(ceil_div(rows, 8), num_sms() * 8);
+  return launch_k(permute_kernel, dim3(blocks), dim3(256), 0, s, (const uint4*)x, ids, sid, T * k,
+                  k, E, rows, vec, (uint4*)xs, pos);
+}
+
+moe_status_t launch_slot_sum(const void* ys, const int32_t* pos, const float* w, int T, int k,
+                             int H, moe_dtype_t dt, int rows, void* out, cudaStream_t s) {
+  const int vec = H * (int)dtype_size(dt) / 16;
+  // rows shorter than a block's pieces get a smaller block
+  const int threads = vec >= 256 ? 256 : std::max(32, ceil_div(vec, 32) * 32);
+  const int parts = ceil_div(vec, threads);
+  if ((int64_t)T * parts > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
+  auto go = [&](auto kern) {
+    return launch_k(kern, dim3((unsigned)(T * parts)), dim3(threads), 0, s, (const uint4*)ys, pos,
+                    w, k, rows, vec, parts, (uint4*)out);
+  };
+  if (dt == MOE_BF16)
+    return w ? go(slot_sum_kernel<__nv_bfloat16, true>) : go(slot_sum_kernel<__nv_bfloat16, false>);
+  return w ? go(slot_sum_kernel<float, true>) : go(slot_sum_kernel<float, false>);
+}
+
+moe_status_t launch_unpermute_backward(const void* dout, const void* ys, const int32_t* sid,
+                                       const int32_t* pos, const float* w, int T, int k, int H,
+                                       moe_dtype_t dt, int rows, void* dys, float* dw,
+                                       cudaStream_t s) {
+  const int vec = H * (int)dtype_size(dt) / 16;
+  const dim3 grid((unsigned)(T + ceil_div(rows, kZeroRows)));
+  if (dt == MOE_BF16)
+    return launch_k(unpermute_backward_kernel<__nv_bfloat16>, grid, dim3(kUbThreads), 0, s,
+                    (const uint4*)dout, (const uint4*)ys, sid, pos, w, T, k, rows, vec,
+                    (uint4*)dys, dw);
+  return launch_k(unpermute_backward_kernel<float>, grid, dim3(kUbThreads), 0, s,
+                  (const uint4*)dout, (const uint4*)ys, sid, pos, w, T, k, rows, vec,
+                  (uint4*)dys, dw);
+}
+
+}  // namespace moe
