@@ -6,6 +6,14 @@ using namespace moe;
 
 namespace {
 
+// bf16 products run on the tensor cores, fp32 ones on the CUDA cores.
+moe_status_t product(ExpertProduct kind, const moe_experts_t& c, const void* a, const void* w,
+                     const float* h13, const int32_t* counts, void* out, void* act,
+                     cudaStream_t s) {
+  return c.dtype == MOE_BF16 ? launch_expert_product_tc(kind, c, a, w, h13, counts, out, act, s)
+                             : launch_expert_product_simt(kind, c, a, w, h13, counts, out, act, s);
+}
+
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
 bool dtype_ok(moe_dtype_t d) { return d == MOE_F32 || d == MOE_BF16; }
@@ -93,7 +101,7 @@ moe_status_t moe_expert_up(const moe_experts_t* cfg, const void* xs, const void*
   const moe_status_t st = check_experts(cfg);
   if (st != MOE_OK) return st;
   if (!rows_ok(xs, W13, h13, act) || !words_ok(counts)) return MOE_ERR_INVALID_ARG;
-  return launch_expert_product_simt(kUp, *cfg, xs, W13, nullptr, counts, h13, act, stream);
+  return product(kUp, *cfg, xs, W13, nullptr, counts, h13, act, stream);
 }
 
 moe_status_t moe_expert_down(const moe_experts_t* cfg, const void* act, const void* W2,
@@ -101,7 +109,7 @@ moe_status_t moe_expert_down(const moe_experts_t* cfg, const void* act, const vo
   const moe_status_t st = check_experts(cfg);
   if (st != MOE_OK) return st;
   if (!rows_ok(act, W2, ys) || !words_ok(counts)) return MOE_ERR_INVALID_ARG;
-  return launch_expert_product_simt(kDown, *cfg, act, W2, nullptr, counts, ys, nullptr, stream);
+  return product(kDown, *cfg, act, W2, nullptr, counts, ys, nullptr, stream);
 }
 
 moe_status_t moe_expert_down_backward(const moe_experts_t* cfg, const void* dys, const void* W2,
@@ -110,7 +118,7 @@ moe_status_t moe_expert_down_backward(const moe_experts_t* cfg, const void* dys,
   const moe_status_t st = check_experts(cfg);
   if (st != MOE_OK) return st;
   if (!rows_ok(dys, W2, h13, dh13, act) || !words_ok(counts)) return MOE_ERR_INVALID_ARG;
-  return launch_expert_product_simt(kDownGrad, *cfg, dys, W2, h13, counts, dh13, act, stream);
+  return product(kDownGrad, *cfg, dys, W2, h13, counts, dh13, act, stream);
 }
 
 moe_status_t moe_expert_up_backward(const moe_experts_t* cfg, const void* dh13, const void* W13,
@@ -118,8 +126,7 @@ moe_status_t moe_expert_up_backward(const moe_experts_t* cfg, const void* dh13, 
   const moe_status_t st = check_experts(cfg);
   if (st != MOE_OK) return st;
   if (!rows_ok(dh13, W13, dxs) || !words_ok(counts)) return MOE_ERR_INVALID_ARG;
-  return launch_expert_product_simt(kUpGrad, *cfg, dh13, W13, nullptr, counts, dxs, nullptr,
-                                    stream);
+  return product(kUpGrad, *cfg, dh13, W13, nullptr, counts, dxs, nullptr, stream);
 }
 
 moe_status_t moe_expert_weight_grad(int rows, int E, int M, int N, moe_dtype_t dtype,
@@ -131,6 +138,8 @@ moe_status_t moe_expert_weight_grad(int rows, int E, int M, int N, moe_dtype_t d
     return MOE_ERR_INVALID_ARG;
   if (E > kMaxExperts || rows > kMaxRows || M > 1 << 21 || N > 1 << 21) return MOE_ERR_UNSUPPORTED;
   if (!rows_ok(dy, a, dW) || !words_ok(counts)) return MOE_ERR_INVALID_ARG;
+  if (dtype == MOE_BF16)
+    return launch_weight_grad_tc(rows, E, M, N, out_dtype, accumulate, dy, a, counts, dW, stream);
   return launch_weight_grad_simt(rows, E, M, N, dtype, out_dtype, accumulate, dy, a, counts, dW,
                                  stream);
 }

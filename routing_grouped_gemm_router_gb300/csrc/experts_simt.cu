@@ -63,7 +63,9 @@ __global__ void __launch_bounds__(kThreads) product_kernel(
   T* out = (T*)out_;
   __shared__ int start[kMaxExperts + 1], cnt[kMaxExperts];
   __shared__ float sA[TK][TM + 4], sB[D][TK][TN + 4];
-  if (threadIdx.x < 32) expert_rows(counts, E, rows, start, cnt, &g_status);
+  load_counts(counts, E, cnt);
+  __syncthreads();
+  if (threadIdx.x < 32) expert_rows(E, rows, start, cnt, &g_status);
   __syncthreads();
   const Tile tl = find_tile(start, cnt, E, rows);
   if (tl.pad <= 0) return;
@@ -144,7 +146,9 @@ __global__ void __launch_bounds__(kThreads) weight_grad_kernel(
   pdl_trigger();
   __shared__ int start[kMaxExperts + 1], cnt[kMaxExperts];
   __shared__ float sA[TK][TM], sB[TK][TN];
-  if (threadIdx.x < 32) expert_rows(counts, E, rows, start, cnt, &g_status);
+  load_counts(counts, E, cnt);
+  __syncthreads();
+  if (threadIdx.x < 32) expert_rows(E, rows, start, cnt, &g_status);
   __syncthreads();
   const int tn = (N + TN - 1) / TN, tm = (M + TM - 1) / TM;
   const int e = blockIdx.x / (tn * tm), rest = blockIdx.x % (tn * tm);
@@ -193,7 +197,7 @@ using namespace esimt;
 
 template <typename T>
 static moe_status_t product(ExpertProduct kind, const moe_experts_t& c, const void* a,
-                            const void* w, const void* h13, const int32_t* counts, void* out,
+                            const void* w, const float* h13, const int32_t* counts, void* out,
                             void* act, cudaStream_t s) {
   const int N = kind == kUp || kind == kDownGrad ? c.I : c.H;
   const int K = kind == kUp || kind == kDownGrad ? c.H : kind == kDown ? c.I : 2 * c.I;
@@ -201,7 +205,7 @@ static moe_status_t product(ExpertProduct kind, const moe_experts_t& c, const vo
   const dim3 grid(2 * ceil_div(c.rows, TM) + c.E, ceil_div(N, TN));
   auto go = [&](auto kern) {
     return launch_k(kern, grid, dim3(kThreads), 0, s, (const T*)a, (const T*)w,
-                    (const float*)h13, counts, c.E, c.rows, N, K, out, (T*)act);
+                    h13, counts, c.E, c.rows, N, K, out, (T*)act);
   };
   switch (kind) {
     case kUp: return go(product_kernel<T, kUp>);
@@ -212,7 +216,7 @@ static moe_status_t product(ExpertProduct kind, const moe_experts_t& c, const vo
 }
 
 moe_status_t launch_expert_product_simt(ExpertProduct kind, const moe_experts_t& c, const void* a,
-                                        const void* w, const void* h13, const int32_t* counts,
+                                        const void* w, const float* h13, const int32_t* counts,
                                         void* out, void* act, cudaStream_t s) {
   return c.dtype == MOE_BF16 ? product<__nv_bfloat16>(kind, c, a, w, h13, counts, out, act, s)
                              : product<float>(kind, c, a, w, h13, counts, out, act, s);
@@ -243,7 +247,8 @@ int train_status_read(int reset) {
     int z = 0;
     cudaMemcpyToSymbol(g_status, &z, sizeof(int));
   }
-  return v;
+  const int t = experts_tc_status_read(reset);
+  return t ? t : v;
 }
 
 }  // namespace moe

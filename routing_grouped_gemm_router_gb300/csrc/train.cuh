@@ -55,17 +55,22 @@ constexpr int kRowBlock = MOE_TRAIN_BLOCK;
 constexpr int kMaxExperts = 512;
 constexpr int kMaxRows = 1 << 28;  // rows of a buffer: the sums below stay in 32 bits
 
+// Counts into shared memory by the whole block; the caller synchronises before expert_rows.
+__device__ __forceinline__ void load_counts(const int32_t* __restrict__ counts, int E, int* cnt) {
+  for (int e = threadIdx.x; e < E; e += blockDim.x) cnt[e] = __ldg(counts + e);
+}
+
 // Where expert e's rows start and how many there are, for all experts, in shared memory:
-// start[e] = sum over lower experts of their counts rounded up to kRowBlock, cut to `rows`.
-// start[E] is the end of the last run. Called by one whole warp; the caller synchronises.
-__device__ __forceinline__ void expert_rows(const int32_t* __restrict__ counts, int E, int rows,
-                                            int* start, int* cnt, int* status) {
+// start[e] = sum over lower experts of their counts (in cnt) rounded up to kRowBlock, both cut to
+// fit in `rows` rows. start[E] is the end of the last run. Called by one whole warp; the caller
+// synchronises.
+__device__ __forceinline__ void expert_rows(int E, int rows, int* start, int* cnt, int* status) {
   const int lane = threadIdx.x & 31;
   int base = 0;
   bool bad = false;
   for (int e0 = 0; e0 < E; e0 += 32) {
     const int e = e0 + lane;
-    int c = e < E ? __ldg(counts + e) : 0;
+    int c = e < E ? cnt[e] : 0;
     if (c < 0 || c > rows) {
       bad = true;
       c = c < 0 ? 0 : rows;
@@ -77,7 +82,7 @@ __device__ __forceinline__ void expert_rows(const int32_t* __restrict__ counts, 
       const int o = __shfl_up_sync(0xffffffffu, inc, off);
       if (lane >= off) inc = min(inc + o, (1 << 30) - 1);
     }
-    int s = min(base + inc - pad, rows);
+    const int s = min(base + inc - pad, rows);
     if (s + c > rows) {
       bad = true;
       c = rows - s;
@@ -107,8 +112,15 @@ moe_status_t launch_unpermute_backward(const void* dout, const void* ys, const i
 // act W2^T; down_grad: dys W2 with the SwiGLU's gradient; up_grad: dh13 W13.
 enum ExpertProduct { kUp = 0, kDown = 1, kDownGrad = 2, kUpGrad = 3 };
 moe_status_t launch_expert_product_simt(ExpertProduct kind, const moe_experts_t& c, const void* a,
-                                        const void* w, const void* h13, const int32_t* counts,
+                                        const void* w, const float* h13, const int32_t* counts,
                                         void* out, void* act, cudaStream_t s);
+moe_status_t launch_expert_product_tc(ExpertProduct kind, const moe_experts_t& c, const void* a,
+                                      const void* w, const float* h13, const int32_t* counts,
+                                      void* out, void* act, cudaStream_t s);
+moe_status_t launch_weight_grad_tc(int rows, int E, int M, int N, moe_dtype_t out_dt,
+                                   int accumulate, const void* dy, const void* a,
+                                   const int32_t* counts, void* dW, cudaStream_t s);
+int experts_tc_status_read(int reset);
 moe_status_t launch_weight_grad_simt(int rows, int E, int M, int N, moe_dtype_t dt,
                                      moe_dtype_t out_dt, int accumulate, const void* dy,
                                      const void* a, const int32_t* counts, void* dW,
