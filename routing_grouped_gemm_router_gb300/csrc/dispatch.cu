@@ -94,12 +94,12 @@ __global__ void __launch_bounds__(256) slot_sum_kernel(const uint4* __restrict__
 }
 
 // ------------------------------------------------- gradients of the weighted sum
-// Blocks 0..T-1: one a token. Its dout row is read once and stays in registers (up to kKeep
-// pieces a thread; longer rows come from L2 again) while the k rows of ys stream past; the dot
-// products of all slots meet in shared memory once, at the end. The blocks after them write
-// zeros into rows of no slot.
+// Blocks 0..T-1: one a token. Its slots are taken four at a time: a thread loads its 16-byte piece
+// of dout and of the four ys rows before it uses any, so that four rows are in flight; the dot
+// products of all slots meet in shared memory once, at the end. (dout comes from L2 again for
+// the next four.) The blocks after them write zeros into rows of no slot.
 constexpr int kUbThreads = 256;
-constexpr int kKeep = 4;
+constexpr int kBatch = 4;
 constexpr int kZeroRows = 64;  // table entries a zeroing block looks at
 
 template <typename T>
@@ -110,11 +110,11 @@ __global__ void __launch_bounds__(kUbThreads) unpermute_backward_kernel(
   pdl_wait();
   pdl_trigger();
   constexpr int W = 16 / sizeof(T);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   if ((int)blockIdx.x >= Tn) {
     const int p0 = ((int)blockIdx.x - Tn) * kZeroRows;
     const uint4 z = make_uint4(0, 0, 0, 0);
-    for (int p = p0 + warp; p < min(p0 + kZeroRows, rows); p += kUbThreads / 32) {
+    for (int p = p0 + warp; p < min(p0 + kZeroRows, rows); p += warps) {
       const int r = sid[p];
       if (r >= 0 && r < Tn * k) continue;
       for (int v = lane; v < vec; v += 32) dys[(int64_t)p * vec + v] = z;
@@ -124,53 +124,52 @@ __global__ void __launch_bounds__(kUbThreads) unpermute_backward_kernel(
   __shared__ float dots[32][kUbThreads / 32];
   const int64_t t = blockIdx.x;
   const uint4* drow = dout + t * vec;
-  uint4 keep[kKeep];
+  for (int j0 = 0; j0 < k; j0 += kBatch) {
+    const uint4* yrow[kBatch];
+    uint4* orow[kBatch];
+    float wj[kBatch], dot[kBatch];
+    bool live[kBatch];
 #pragma unroll
-  for (int i = 0; i < kKeep; ++i) {
-    const int v = threadIdx.x + i * kUbThreads;
-    if (v < vec) keep[i] = drow[v];
-  }
-  for (int j = 0; j < k; ++j) {
-    const int p = __ldg(pos + t * k + j);
-    const bool live = p >= 0 && p < rows;
-    float dot = 0.f;
-    if (live) {
-      const float wj = __ldg(w + t * k + j);
-      const uint4* yrow = ys + (int64_t)p * vec;
-      uint4* orow = dys + (int64_t)p * vec;
-      auto piece = [&](const uint4& dq, const uint4& yq, int v) {
-        float d[W], y[W];
-        Vec<T>::unpack(dq, d);
-        Vec<T>::unpack(yq, y);
+    for (int j = 0; j < kBatch; ++j) {
+      const int p = j0 + j < k ? __ldg(pos + t * k + j0 + j) : -1;
+      live[j] = p >= 0 && p < rows;
+      wj[j] = live[j] ? __ldg(w + t * k + j0 + j) : 0.f;
+      const int64_t at = (int64_t)(live[j] ? p : 0) * vec;
+      yrow[j] = ys + at;
+      orow[j] = dys + at;
+      dot[j] = 0.f;
+    }
+    for (int v = threadIdx.x; v < vec; v += blockDim.x) {
+      const uint4 dq = drow[v];
+      uint4 yq[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+        if (live[j]) yq[j] = __ldcs(yrow[j] + v);
+      float d[W];
+      Vec<T>::unpack(dq, d);
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        if (!live[j]) continue;
+        float y[W];
+        Vec<T>::unpack(yq[j], y);
 #pragma unroll
         for (int i = 0; i < W; ++i) {
-          dot = fmaf(d[i], y[i], dot);
-          d[i] *= wj;
+          dot[j] = fmaf(d[i], y[i], dot[j]);
+          y[i] = d[i] * wj[j];
         }
-        orow[v] = Vec<T>::pack(d);
-      };
-      uint4 yq[kKeep];
-#pragma unroll
-      for (int i = 0; i < kKeep; ++i) {
-        const int v = threadIdx.x + i * kUbThreads;
-        if (v < vec) yq[i] = __ldcs(yrow + v);
+        orow[j][v] = Vec<T>::pack(y);
       }
-#pragma unroll
-      for (int i = 0; i < kKeep; ++i) {
-        const int v = threadIdx.x + i * kUbThreads;
-        if (v < vec) piece(keep[i], yq[i], v);
-      }
-      for (int v = threadIdx.x + kKeep * kUbThreads; v < vec; v += kUbThreads)
-        piece(drow[v], __ldcs(yrow + v), v);
     }
-    dot = warp_total(dot);
-    if (lane == 0) dots[j][warp] = dot;
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const float s = warp_total(dot[j]);
+      if (lane == 0 && j0 + j < k) dots[j0 + j][warp] = s;
+    }
   }
   __syncthreads();
   if (threadIdx.x < k) {
     float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < kUbThreads / 32; ++i) s += dots[threadIdx.x][i];
+    for (int i = 0; i < warps; ++i) s += dots[threadIdx.x][i];
     dw[t * k + threadIdx.x] = s;
   }
 }
@@ -210,11 +209,12 @@ moe_status_t launch_unpermute_backward(const void* dout, const void* ys, const i
                                        cudaStream_t s) {
   const int vec = H * (int)dtype_size(dt) / 16;
   const dim3 grid((unsigned)(T + ceil_div(rows, kZeroRows)));
+  const int threads = std::max(32, std::min(kUbThreads, ceil_div(vec, 32) * 32));
   if (dt == MOE_BF16)
-    return launch_k(unpermute_backward_kernel<__nv_bfloat16>, grid, dim3(kUbThreads), 0, s,
+    return launch_k(unpermute_backward_kernel<__nv_bfloat16>, grid, dim3(threads), 0, s,
                     (const uint4*)dout, (const uint4*)ys, sid, pos, w, T, k, rows, vec,
                     (uint4*)dys, dw);
-  return launch_k(unpermute_backward_kernel<float>, grid, dim3(kUbThreads), 0, s,
+  return launch_k(unpermute_backward_kernel<float>, grid, dim3(threads), 0, s,
                   (const uint4*)dout, (const uint4*)ys, sid, pos, w, T, k, rows, vec,
                   (uint4*)dys, dw);
 }

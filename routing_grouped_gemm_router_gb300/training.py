@@ -12,34 +12,86 @@ run is padded to 16 rows; rows of no slot are zeros.
 """
 from __future__ import annotations
 
+import ctypes
 from typing import NamedTuple, Optional
 
 import torch
 
 from . import _lib as L
 
-_DTYPES = {torch.bfloat16: L.MOE_BF16, torch.float32: L.MOE_F32}
+_C = L.lib()
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+_DTYPES = {_BF16: L.MOE_BF16, _F32: L.MOE_F32}
+_empty, _empty_like, _byref = torch.empty, torch.empty_like, ctypes.byref
 
 
-def _need(ok, what):
-    if not ok:
-        raise ValueError(what)
+# The checks run on every call of operators that take a few microseconds, so a good tensor
+# passes in one expression and only a bad one is described.
+def _refuse(name, t, shape, dtype):
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name}: a tensor is needed, got {type(t).__name__}")
+    if (t.dtype not in _DTYPES) if dtype is None else (t.dtype != dtype):
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype or 'bfloat16 or float32'}")
+    if t.dim() != len(shape) or any(a is not None and a != b for a, b in zip(shape, t.shape)):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: has to be contiguous (strides {t.stride()})")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: has to be on a CUDA device")
+    raise ValueError(f"{name}: is on {t.device}, not on the device of the other tensors")
 
 
-def _rows(name, t, shape, dtype=None):
-    """A contiguous bf16 or fp32 CUDA tensor of `shape` (None: any extent)."""
-    _need(isinstance(t, torch.Tensor), f"{name}: a tensor is needed")
-    _need(t.dtype in _DTYPES if dtype is None else t.dtype == dtype,
-          f"{name}: dtype {t.dtype}, expected {dtype or 'bfloat16 or float32'}")
-    _need(t.dim() == len(shape) and all(a is None or a == b for a, b in zip(shape, t.shape)),
-          f"{name}: shape {tuple(t.shape)}, expected {shape}")
-    _need(t.is_contiguous(), f"{name}: has to be contiguous (strides {t.stride()})")
-    _need(t.is_cuda, f"{name}: has to be on a CUDA device")
-    return t
+def _first(name, t):
+    """The first tensor of a call, bf16 or fp32 [a, b]: its two extents and device."""
+    try:
+        if t.dtype in _DTYPES and t.is_contiguous() and t.is_cuda:
+            a, b = t.shape
+            return a, b, t.get_device()
+    except (AttributeError, ValueError):
+        pass
+    _refuse(name, t, (None, None), None)
 
 
-def _ints(name, t, shape):
-    return _rows(name, t, shape, torch.int32)
+def _like(name, t, shape, dtype, dev):
+    """A further tensor: this very shape, type and device."""
+    try:
+        if t.shape == shape and t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+            return
+    except AttributeError:
+        pass
+    _refuse(name, t, shape, dtype)
+
+
+def _any2(name, t, dtype, dev, rows=None):
+    """A further tensor [rows or any, any] of this type: its two extents."""
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+            a, b = t.shape
+            if rows is None or a == rows:
+                return a, b
+    except (AttributeError, ValueError):
+        pass
+    _refuse(name, t, (rows, None), dtype)
+
+
+def _weights(name, t, shape, dtype, dev):
+    """Expert weights: three extents, those of `shape` that are not None given."""
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and t.dim() == 3 and \
+                all(a is None or a == b for a, b in zip(shape, t.shape)):
+            return t.shape
+    except AttributeError:
+        pass
+    _refuse(name, t, shape, dtype)
+
+
+def _stream(dev):
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _done(fn, status):
+    if status:
+        raise L.MoeError(fn, status)
 
 
 def buffer_rows(T: int, k: int, E: int) -> int:
@@ -58,126 +110,137 @@ class SortedTokens(NamedTuple):
 def sort_tokens(topk_ids, E: int) -> SortedTokens:
     """The table of the routed slots sorted by expert (``moe_align`` with 16-row blocks).
     Ids outside [0, E) are dropped (and recorded in the device status)."""
-    _ints("topk_ids", topk_ids, (None, None))
-    T, k = topk_ids.shape
+    dev = topk_ids.get_device() if isinstance(topk_ids, torch.Tensor) else -1
+    T, k = _any2("topk_ids", topk_ids, _I32, dev)
+    if dev < 0:
+        _refuse("topk_ids", topk_ids, (None, None), _I32)
     P = buffer_rows(T, k, E)
-    _need(P > 0 and E >= k, f"topk_ids: {T} tokens, {k} of {E} experts")
+    if P <= 0 or E < k:
+        raise ValueError(f"topk_ids: {T} tokens, {k} of {E} experts")
     ws_bytes = L.moe_align_workspace_size(T, k, E, L.MOE_TRAIN_BLOCK)
-    blocks = P // L.MOE_TRAIN_BLOCK
+    blocks, words = P // L.MOE_TRAIN_BLOCK, (ws_bytes + 3) // 4
     # one allocation: sorted_ids, then expert_ids, counts and the total, then scratch
-    buf = torch.empty(P + blocks + E + 1 + (ws_bytes + 3) // 4, dtype=torch.int32,
-                      device=topk_ids.device)
-    sid, eid, counts, npp, ws = buf.split([P, blocks, E, 1, buf.numel() - P - blocks - E - 1])
-    L.moe_align(topk_ids, T, k, E, L.MOE_TRAIN_BLOCK, sid, eid, npp, counts,
-                ws if ws_bytes else None, ws_bytes)
+    buf = _empty(P + blocks + E + 1 + words, dtype=_I32, device=topk_ids.device)
+    sid, eid, counts, npp, ws = buf.split([P, blocks, E, 1, words])
+    p = buf.data_ptr()
+    _done("moe_align", _C.moe_align(
+        topk_ids.data_ptr(), T, k, E, L.MOE_TRAIN_BLOCK, p, p + 4 * P, p + 4 * (P + blocks + E),
+        p + 4 * (P + blocks), p + 4 * (P + blocks + E + 1) if words else None, ws_bytes,
+        _stream(dev)))
     return SortedTokens(sid, eid, npp, counts)
 
 
 def permute(x, topk_ids, sorted_ids, E: int):
     """(xs[rows, H], row_pos[T, k]): token rows copied to their slots' rows; -1 for dropped slots."""
-    _rows("x", x, (None, None))
-    T, H = x.shape
-    _ints("topk_ids", topk_ids, (T, None))
-    _ints("sorted_ids", sorted_ids, (None,))
-    k, P = topk_ids.shape[1], sorted_ids.shape[0]
-    xs = torch.empty(P, H, dtype=x.dtype, device=x.device)
-    pos = torch.empty(T, k, dtype=torch.int32, device=x.device)
-    L.moe_permute(x, topk_ids, sorted_ids, T, k, E, H, _DTYPES[x.dtype], P, xs, pos)
+    T, H, dev = _first("x", x)
+    k = _any2("topk_ids", topk_ids, _I32, dev, T)[1]
+    P = sorted_ids.shape[0]
+    _like("sorted_ids", sorted_ids, (P,), _I32, dev)
+    xs = _empty(P, H, dtype=x.dtype, device=x.device)
+    pos = _empty_like(topk_ids)
+    _done("moe_permute", _C.moe_permute(
+        x.data_ptr(), topk_ids.data_ptr(), sorted_ids.data_ptr(), T, k, E, H, _DTYPES[x.dtype], P,
+        xs.data_ptr(), pos.data_ptr(), _stream(dev)))
     return xs, pos
 
 
 def permute_backward(dxs, row_pos):
     """dx[T, H]: the gradients of a token's rows summed over its slots."""
-    _rows("dxs", dxs, (None, None))
-    _ints("row_pos", row_pos, (None, None))
-    (P, H), (T, k) = dxs.shape, row_pos.shape
-    dx = torch.empty(T, H, dtype=dxs.dtype, device=dxs.device)
-    L.moe_permute_backward(dxs, row_pos, T, k, H, _DTYPES[dxs.dtype], P, dx)
+    P, H, dev = _first("dxs", dxs)
+    T, k = _any2("row_pos", row_pos, _I32, dev)
+    dx = _empty(T, H, dtype=dxs.dtype, device=dxs.device)
+    _done("moe_permute_backward", _C.moe_permute_backward(
+        dxs.data_ptr(), row_pos.data_ptr(), T, k, H, _DTYPES[dxs.dtype], P, dx.data_ptr(),
+        _stream(dev)))
     return dx
 
 
 def unpermute(ys, row_pos, topk_w):
     """out[T, H]: the rows of a token's slots, weighted and summed."""
-    _rows("ys", ys, (None, None))
-    _ints("row_pos", row_pos, (None, None))
-    (P, H), (T, k) = ys.shape, row_pos.shape
-    _rows("topk_w", topk_w, (T, k), torch.float32)
-    out = torch.empty(T, H, dtype=ys.dtype, device=ys.device)
-    L.moe_unpermute(ys, row_pos, topk_w, T, k, H, _DTYPES[ys.dtype], P, out)
+    P, H, dev = _first("ys", ys)
+    T, k = _any2("row_pos", row_pos, _I32, dev)
+    _like("topk_w", topk_w, (T, k), _F32, dev)
+    out = _empty(T, H, dtype=ys.dtype, device=ys.device)
+    _done("moe_unpermute", _C.moe_unpermute(
+        ys.data_ptr(), row_pos.data_ptr(), topk_w.data_ptr(), T, k, H, _DTYPES[ys.dtype], P,
+        out.data_ptr(), _stream(dev)))
     return out
 
 
 def unpermute_backward(dout, ys, sorted_ids, row_pos, topk_w):
     """(dys[rows, H], dtopk_w[T, k]) of ``unpermute``."""
-    _rows("ys", ys, (None, None))
-    _ints("row_pos", row_pos, (None, None))
-    (P, H), (T, k) = ys.shape, row_pos.shape
-    _rows("dout", dout, (T, H), ys.dtype)
-    _ints("sorted_ids", sorted_ids, (P,))
-    _rows("topk_w", topk_w, (T, k), torch.float32)
-    dys, dw = torch.empty_like(ys), torch.empty_like(topk_w)
-    L.moe_unpermute_backward(dout, ys, sorted_ids, row_pos, topk_w, T, k, H, _DTYPES[ys.dtype],
-                             P, dys, dw)
+    P, H, dev = _first("ys", ys)
+    T, k = _any2("row_pos", row_pos, _I32, dev)
+    _like("dout", dout, (T, H), ys.dtype, dev)
+    _like("sorted_ids", sorted_ids, (P,), _I32, dev)
+    _like("topk_w", topk_w, (T, k), _F32, dev)
+    dys, dw = _empty_like(ys), _empty_like(topk_w)
+    _done("moe_unpermute_backward", _C.moe_unpermute_backward(
+        dout.data_ptr(), ys.data_ptr(), sorted_ids.data_ptr(), row_pos.data_ptr(),
+        topk_w.data_ptr(), T, k, H, _DTYPES[ys.dtype], P, dys.data_ptr(), dw.data_ptr(),
+        _stream(dev)))
     return dys, dw
 
 
 # -------------------------------------------------------------------------------- experts
 def _experts_cfg(P, E, H, I, dtype):
-    return L.moe_experts_t(P, E, H, I, _DTYPES[dtype])
+    return _byref(L.moe_experts_t(P, E, H, I, _DTYPES[dtype]))
 
 
 def expert_up(xs, W13, counts):
     """(h13[rows, 2I], act[rows, I]): gate and up projections (fp32, kept for the backward pass) and
     silu(gate) * up of every expert's rows."""
-    _rows("xs", xs, (None, None))
-    P, H = xs.shape
-    _rows("W13", W13, (None, None, H), xs.dtype)
-    E, I2 = W13.shape[:2]
-    _need(I2 % 2 == 0, f"W13: {I2} rows are no gate and up halves")
-    _ints("counts", counts, (E,))
-    h13 = torch.empty(P, I2, dtype=torch.float32, device=xs.device)
-    act = torch.empty(P, I2 // 2, dtype=xs.dtype, device=xs.device)
-    L.moe_expert_up(_experts_cfg(P, E, H, I2 // 2, xs.dtype), xs, W13, counts, h13, act)
+    P, H, dev = _first("xs", xs)
+    E, I2, _ = _weights("W13", W13, (None, None, H), xs.dtype, dev)
+    if I2 % 2:
+        raise ValueError(f"W13: {I2} rows are no gate and up halves")
+    _like("counts", counts, (E,), _I32, dev)
+    h13 = _empty(P, I2, dtype=_F32, device=xs.device)
+    act = _empty(P, I2 // 2, dtype=xs.dtype, device=xs.device)
+    _done("moe_expert_up", _C.moe_expert_up(
+        _experts_cfg(P, E, H, I2 // 2, xs.dtype), xs.data_ptr(), W13.data_ptr(),
+        counts.data_ptr(), h13.data_ptr(), act.data_ptr(), _stream(dev)))
     return h13, act
 
 
 def expert_down(act, W2, counts):
     """ys[rows, H]: the down projection of every expert's rows, without the router weight."""
-    _rows("act", act, (None, None))
-    P, I = act.shape
-    _rows("W2", W2, (None, None, I), act.dtype)
-    E, H = W2.shape[:2]
-    _ints("counts", counts, (E,))
-    ys = torch.empty(P, H, dtype=act.dtype, device=act.device)
-    L.moe_expert_down(_experts_cfg(P, E, H, I, act.dtype), act, W2, counts, ys)
+    P, I, dev = _first("act", act)
+    E, H, _ = _weights("W2", W2, (None, None, I), act.dtype, dev)
+    _like("counts", counts, (E,), _I32, dev)
+    ys = _empty(P, H, dtype=act.dtype, device=act.device)
+    _done("moe_expert_down", _C.moe_expert_down(
+        _experts_cfg(P, E, H, I, act.dtype), act.data_ptr(), W2.data_ptr(), counts.data_ptr(),
+        ys.data_ptr(), _stream(dev)))
     return ys
 
 
 def expert_down_backward(dys, W2, h13, counts):
     """(dh13[rows, 2I], act[rows, I]): the gradient through the down projection and the SwiGLU, and
     the activations computed again for the gradient of W2."""
-    _rows("dys", dys, (None, None))
-    P, H = dys.shape
-    _rows("W2", W2, (None, H, None), dys.dtype)
-    E, I = W2.shape[0], W2.shape[2]
-    _rows("h13", h13, (P, 2 * I), torch.float32)
-    _ints("counts", counts, (E,))
-    dh13 = torch.empty(P, 2 * I, dtype=dys.dtype, device=dys.device)
-    act = torch.empty(P, I, dtype=dys.dtype, device=dys.device)
-    L.moe_expert_down_backward(_experts_cfg(P, E, H, I, dys.dtype), dys, W2, h13, counts, dh13, act)
+    P, H, dev = _first("dys", dys)
+    E, _, I = _weights("W2", W2, (None, H, None), dys.dtype, dev)
+    _like("h13", h13, (P, 2 * I), _F32, dev)
+    _like("counts", counts, (E,), _I32, dev)
+    dh13 = _empty(P, 2 * I, dtype=dys.dtype, device=dys.device)
+    act = _empty(P, I, dtype=dys.dtype, device=dys.device)
+    _done("moe_expert_down_backward", _C.moe_expert_down_backward(
+        _experts_cfg(P, E, H, I, dys.dtype), dys.data_ptr(), W2.data_ptr(), h13.data_ptr(),
+        counts.data_ptr(), dh13.data_ptr(), act.data_ptr(), _stream(dev)))
     return dh13, act
 
 
 def expert_up_backward(dh13, W13, counts):
     """dxs[rows, H]: the gradient through the gate and up projections."""
-    _rows("dh13", dh13, (None, None))
-    P, I2 = dh13.shape
-    _rows("W13", W13, (None, I2, None), dh13.dtype)
-    _need(I2 % 2 == 0, f"dh13: {I2} columns are no gate and up halves")
-    E, H = W13.shape[0], W13.shape[2]
-    _ints("counts", counts, (E,))
-    dxs = torch.empty(P, H, dtype=dh13.dtype, device=dh13.device)
-    L.moe_expert_up_backward(_experts_cfg(P, E, H, I2 // 2, dh13.dtype), dh13, W13, counts, dxs)
+    P, I2, dev = _first("dh13", dh13)
+    E, _, H = _weights("W13", W13, (None, I2, None), dh13.dtype, dev)
+    if I2 % 2:
+        raise ValueError(f"dh13: {I2} columns are no gate and up halves")
+    _like("counts", counts, (E,), _I32, dev)
+    dxs = _empty(P, H, dtype=dh13.dtype, device=dh13.device)
+    _done("moe_expert_up_backward", _C.moe_expert_up_backward(
+        _experts_cfg(P, E, H, I2 // 2, dh13.dtype), dh13.data_ptr(), W13.data_ptr(),
+        counts.data_ptr(), dxs.data_ptr(), _stream(dev)))
     return dxs
 
 
@@ -186,63 +249,69 @@ def expert_weight_grad(dy, a, counts, out: Optional[torch.Tensor] = None,
     """dW[E, M, N] = dy_e^T a_e over every expert's rows: W2's gradient from (dys, act), W13's from
     (dh13, xs). `out` (then its dtype counts) is overwritten, or added to with `accumulate`;
     otherwise a new tensor of out_dtype (default: dy's) is returned."""
-    _rows("dy", dy, (None, None))
-    P, M = dy.shape
-    _rows("a", a, (P, None), dy.dtype)
-    _ints("counts", counts, (None,))
-    E, N = counts.shape[0], a.shape[1]
+    P, M, dev = _first("dy", dy)
+    N = _any2("a", a, dy.dtype, dev, P)[1]
+    E = counts.numel()
+    _like("counts", counts, (E,), _I32, dev)
     if out is None:
-        _need(not accumulate, "accumulate: needs the tensor to add to (out)")
-        out = torch.empty(E, M, N, dtype=out_dtype or dy.dtype, device=dy.device)
-    _rows("out", out, (E, M, N), out_dtype)
-    L.moe_expert_weight_grad(P, E, M, N, _DTYPES[dy.dtype], _DTYPES[out.dtype], accumulate, dy, a,
-                             counts, out)
+        if accumulate:
+            raise ValueError("accumulate: needs the tensor to add to (out)")
+        out = _empty(E, M, N, dtype=out_dtype or dy.dtype, device=dy.device)
+    _like("out", out, (E, M, N), out_dtype or out.dtype, dev)
+    if out.dtype not in _DTYPES:
+        _refuse("out", out, (E, M, N), None)
+    _done("moe_expert_weight_grad", _C.moe_expert_weight_grad(
+        P, E, M, N, _DTYPES[dy.dtype], _DTYPES[out.dtype], int(bool(accumulate)), dy.data_ptr(),
+        a.data_ptr(), counts.data_ptr(), out.data_ptr(), _stream(dev)))
     return out
 
 
 # -------------------------------------------------------------------- norms around the block
-def _gate_kind(gate, T, H, dtype):
+def _gate_kind(gate, T, H, dtype, dev):
     if gate is None:
         return L.MOE_GATE_NONE
-    shape = tuple(gate.shape)
-    if shape == (H,):
-        _rows("gate", gate, (H,), torch.float32)
+    if gate.shape == (H,):
+        _like("gate", gate, (H,), _F32, dev)
         return L.MOE_GATE_CHANNEL
-    if shape == (T, 1):
-        _rows("gate", gate, (T, 1), torch.float32)
+    if gate.shape == (T, 1):
+        _like("gate", gate, (T, 1), _F32, dev)
         return L.MOE_GATE_TOKEN
-    _rows("gate", gate, (T, H), dtype)
+    _like("gate", gate, (T, H), dtype, dev)
     return L.MOE_GATE_FULL
 
 
 def _block_ws(cfg, device):
-    n = L.moe_block_workspace_size(cfg)
-    return torch.empty(n, dtype=torch.uint8, device=device), n
+    n = ctypes.c_size_t(0)
+    _done("moe_block_workspace_size", _C.moe_block_workspace_size(_byref(cfg), _byref(n)))
+    return _empty(n.value, dtype=torch.uint8, device=device), n.value
 
 
 def block_norm(x, gamma, eps: float = 1e-6, offset: float = 0.0):
     """(h, rstd): x * rstd * (offset + gamma), rstd = (mean(x^2) + eps)^-1/2 of each row."""
-    _rows("x", x, (None, None))
-    T, H = x.shape
-    _rows("gamma", gamma, (H,), torch.float32)
-    h, rstd = torch.empty_like(x), torch.empty(T, dtype=torch.float32, device=x.device)
-    L.moe_block_norm(L.moe_block_t(T, H, _DTYPES[x.dtype], 0, 1.0, offset, eps), x, gamma, h, rstd)
+    T, H, dev = _first("x", x)
+    _like("gamma", gamma, (H,), _F32, dev)
+    h, rstd = _empty_like(x), _empty(T, dtype=_F32, device=x.device)
+    cfg = L.moe_block_t(T, H, _DTYPES[x.dtype], 0, 1.0, offset, eps)
+    _done("moe_block_norm", _C.moe_block_norm(
+        _byref(cfg), x.data_ptr(), gamma.data_ptr(), h.data_ptr(), rstd.data_ptr(), _stream(dev)))
     return h, rstd
 
 
 def block_norm_backward(dh, x, gamma, rstd, dres=None, offset: float = 0.0):
     """(dx, dgamma) of ``block_norm``; dres, the gradient that reaches x past the norm, is added."""
-    _rows("x", x, (None, None))
-    T, H = x.shape
-    _rows("dh", dh, (T, H), x.dtype)
-    _rows("gamma", gamma, (H,), torch.float32)
-    _rows("rstd", rstd, (T,), torch.float32)
+    T, H, dev = _first("x", x)
+    _like("dh", dh, (T, H), x.dtype, dev)
+    _like("gamma", gamma, (H,), _F32, dev)
+    _like("rstd", rstd, (T,), _F32, dev)
     if dres is not None:
-        _rows("dres", dres, (T, H), x.dtype)
+        _like("dres", dres, (T, H), x.dtype, dev)
     cfg = L.moe_block_t(T, H, _DTYPES[x.dtype], 0, 1.0, offset, 0.0)
     ws, n = _block_ws(cfg, x.device)
-    dx, dgamma = torch.empty_like(x), torch.empty_like(gamma)
-    L.moe_block_norm_backward(cfg, dh, x, gamma, rstd, dres, dx, dgamma, ws, n)
+    dx, dgamma = _empty_like(x), _empty_like(gamma)
+    _done("moe_block_norm_backward", _C.moe_block_norm_backward(
+        _byref(cfg), dh.data_ptr(), x.data_ptr(), gamma.data_ptr(), rstd.data_ptr(),
+        dres.data_ptr() if dres is not None else None, dx.data_ptr(), dgamma.data_ptr(),
+        ws.data_ptr(), n, _stream(dev)))
     return dx, dgamma
 
 
@@ -257,18 +326,21 @@ def block_join(x, y, gamma, gate=None, scale: float = 1.0, gamma_next=None, eps:
                offset: float = 0.0) -> Joined:
     """out = x + scale * gate * norm(y; gamma), and h = norm(out; gamma_next) of the same pass.
     gate: None, fp32 [H] (a channel), fp32 [T, 1] (a token) or [T, H] of x's dtype."""
-    _rows("x", x, (None, None))
-    T, H = x.shape
-    _rows("y", y, (T, H), x.dtype)
-    _rows("gamma", gamma, (H,), torch.float32)
-    kind = _gate_kind(gate, T, H, x.dtype)
-    out, rstd_y = torch.empty_like(x), torch.empty(T, dtype=torch.float32, device=x.device)
+    T, H, dev = _first("x", x)
+    _like("y", y, (T, H), x.dtype, dev)
+    _like("gamma", gamma, (H,), _F32, dev)
+    kind = _gate_kind(gate, T, H, x.dtype, dev)
+    out, rstd_y = _empty_like(x), _empty(T, dtype=_F32, device=x.device)
     h = rstd_out = None
     if gamma_next is not None:
-        _rows("gamma_next", gamma_next, (H,), torch.float32)
-        h, rstd_out = torch.empty_like(x), torch.empty_like(rstd_y)
-    L.moe_block_join(L.moe_block_t(T, H, _DTYPES[x.dtype], kind, scale, offset, eps), x, y, gamma,
-                     gate, gamma_next, out, rstd_y, h, rstd_out)
+        _like("gamma_next", gamma_next, (H,), _F32, dev)
+        h, rstd_out = _empty_like(x), _empty_like(rstd_y)
+    cfg = L.moe_block_t(T, H, _DTYPES[x.dtype], kind, scale, offset, eps)
+    nxt = h is not None
+    _done("moe_block_join", _C.moe_block_join(
+        _byref(cfg), x.data_ptr(), y.data_ptr(), gamma.data_ptr(), gate.data_ptr() if kind else None,
+        gamma_next.data_ptr() if nxt else None, out.data_ptr(), rstd_y.data_ptr(),
+        h.data_ptr() if nxt else None, rstd_out.data_ptr() if nxt else None, _stream(dev)))
     return Joined(out, rstd_y, h, rstd_out)
 
 
@@ -284,29 +356,35 @@ def block_join_backward(dres, y, gamma, rstd_y, gate=None, scale: float = 1.0, d
                         gamma_next=None, rstd_out=None, offset: float = 0.0) -> JoinGrads:
     """Gradients of ``block_join``. dres: the gradient of `out` from past the next norm (None: no
     such path); dh, out, gamma_next, rstd_out: the next norm's, when the join had one."""
-    _rows("y", y, (None, None))
-    T, H = y.shape
-    _rows("gamma", gamma, (H,), torch.float32)
-    _rows("rstd_y", rstd_y, (T,), torch.float32)
+    T, H, dev = _first("y", y)
+    _like("gamma", gamma, (H,), _F32, dev)
+    _like("rstd_y", rstd_y, (T,), _F32, dev)
     if dres is not None:
-        _rows("dres", dres, (T, H), y.dtype)
-    given = [t is not None for t in (dh, out, gamma_next, rstd_out)]
-    _need(all(given) or not any(given), "dh, out, gamma_next and rstd_out are given together")
-    _need(dres is not None or dh is not None, "dres or dh: a gradient is needed")
+        _like("dres", dres, (T, H), y.dtype, dev)
+    nxt = dh is not None
+    if any((t is not None) != nxt for t in (out, gamma_next, rstd_out)):
+        raise ValueError("dh, out, gamma_next and rstd_out are given together")
+    if dres is None and not nxt:
+        raise ValueError("dres or dh: a gradient is needed")
     dgn = None
-    if dh is not None:
-        _rows("dh", dh, (T, H), y.dtype)
-        _rows("out", out, (T, H), y.dtype)
-        _rows("gamma_next", gamma_next, (H,), torch.float32)
-        _rows("rstd_out", rstd_out, (T,), torch.float32)
-        dgn = torch.empty_like(gamma_next)
-    kind = _gate_kind(gate, T, H, y.dtype)
-    dgate = torch.empty_like(gate) if gate is not None else None
+    if nxt:
+        _like("dh", dh, (T, H), y.dtype, dev)
+        _like("out", out, (T, H), y.dtype, dev)
+        _like("gamma_next", gamma_next, (H,), _F32, dev)
+        _like("rstd_out", rstd_out, (T,), _F32, dev)
+        dgn = _empty_like(gamma_next)
+    kind = _gate_kind(gate, T, H, y.dtype, dev)
+    dgate = _empty_like(gate) if kind else None
     cfg = L.moe_block_t(T, H, _DTYPES[y.dtype], kind, scale, offset, 0.0)
     ws, n = _block_ws(cfg, y.device)
-    dx, dy, dg = torch.empty_like(y), torch.empty_like(y), torch.empty_like(gamma)
-    L.moe_block_join_backward(cfg, dres, dh, out, y, gamma, gate, gamma_next, rstd_y, rstd_out, dx,
-                              dy, dg, dgn, dgate, ws, n)
+    dx, dy, dg = _empty_like(y), _empty_like(y), _empty_like(gamma)
+    _done("moe_block_join_backward", _C.moe_block_join_backward(
+        _byref(cfg), dres.data_ptr() if dres is not None else None, dh.data_ptr() if nxt else None,
+        out.data_ptr() if nxt else None, y.data_ptr(), gamma.data_ptr(),
+        gate.data_ptr() if kind else None, gamma_next.data_ptr() if nxt else None,
+        rstd_y.data_ptr(), rstd_out.data_ptr() if nxt else None, dx.data_ptr(), dy.data_ptr(),
+        dg.data_ptr(), dgn.data_ptr() if nxt else None, dgate.data_ptr() if kind else None,
+        ws.data_ptr(), n, _stream(dev)))
     return JoinGrads(dx, dy, dg, dgn, dgate)
 
 
@@ -315,15 +393,19 @@ def route_backward(logits, topk_ids, dtopk_w, mode: int = L.MOE_ROUTE_SOFTMAX,
                    renormalize: bool = True, scale: float = 1.0, logit_bias=None,
                    n_shared: int = 0):
     """dlogits[T, E] from the gradient of ``moe_route``'s topk_w, for the ids it chose."""
-    _rows("logits", logits, (None, None), torch.float32)
-    T, E = logits.shape
-    _ints("topk_ids", topk_ids, (T, None))
-    slots = topk_ids.shape[1]
-    _rows("dtopk_w", dtopk_w, (T, slots), torch.float32)
+    dev = logits.get_device() if isinstance(logits, torch.Tensor) else -1
+    T, E = _any2("logits", logits, _F32, dev)
+    if dev < 0:
+        _refuse("logits", logits, (None, None), _F32)
+    slots = _any2("topk_ids", topk_ids, _I32, dev, T)[1]
+    _like("dtopk_w", dtopk_w, (T, slots), _F32, dev)
     if logit_bias is not None:
-        _rows("logit_bias", logit_bias, (E,), torch.float32)
-    cfg = L.make_config(T, 8, 8, E, slots - n_shared, L.MOE_F32, mode, renormalize, scale,
-                        logit_bias=logit_bias, n_shared=n_shared)
-    dlogits = torch.empty_like(logits)
-    L.moe_route_backward(cfg, logits, topk_ids, dtopk_w, dlogits)
+        _like("logit_bias", logit_bias, (E,), _F32, dev)
+    cfg = L.moe_config_t(T=T, E=E, k=slots - n_shared, mode=mode, renormalize=int(bool(renormalize)),
+                         scale=scale, n_shared=n_shared,
+                         logit_bias=logit_bias.data_ptr() if logit_bias is not None else None)
+    dlogits = _empty_like(logits)
+    _done("moe_route_backward", _C.moe_route_backward(
+        _byref(cfg), logits.data_ptr(), topk_ids.data_ptr(), dtopk_w.data_ptr(),
+        dlogits.data_ptr(), _stream(dev)))
     return dlogits
