@@ -247,8 +247,8 @@ int train_status_read(int reset) {
     int z = 0;
     cudaMemcpyToSymbol(g_status, &z, sizeof(int));
   }
-  const int t = experts_tc_status_read(reset), n = block_norm_status_read(reset);
-  return t ? t : (n ? n : v);
+  const int t = experts_tc_status_read(reset);
+  return t ? t : v;
 }
 
 }  // namespace moe

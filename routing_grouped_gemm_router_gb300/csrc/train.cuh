@@ -133,7 +133,6 @@ struct BlockNormArgs {  // pointers of the forward and backward norm and join ke
   float *rstd_y, *rstd_out, *dgamma, *dgamma_next;
   float* ws;
 };
-int block_norm_status_read(int reset);
 size_t block_norm_ws_bytes(const moe_block_t& c);
 moe_status_t launch_block_norm(const moe_block_t& c, const BlockNormArgs& a, cudaStream_t s);
 moe_status_t launch_block_join(const moe_block_t& c, const BlockNormArgs& a, cudaStream_t s);
