@@ -140,8 +140,7 @@ moe_status_t moe_expert_weight_grad(int rows, int E, int M, int N, moe_dtype_t d
   if (!rows_ok(dy, a, dW) || !words_ok(counts)) return MOE_ERR_INVALID_ARG;
   if (dtype == MOE_BF16)
     return launch_weight_grad_tc(rows, E, M, N, out_dtype, accumulate, dy, a, counts, dW, stream);
-  return launch_weight_grad_simt(rows, E, M, N, dtype, out_dtype, accumulate, dy, a, counts, dW,
-                                 stream);
+  return launch_weight_grad_simt(rows, E, M, N, accumulate, dy, a, counts, dW, stream);
 }
 
 moe_status_t moe_block_workspace_size(const moe_block_t* cfg, size_t* bytes) {

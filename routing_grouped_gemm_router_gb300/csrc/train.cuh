@@ -121,10 +121,9 @@ moe_status_t launch_weight_grad_tc(int rows, int E, int M, int N, moe_dtype_t ou
                                    int accumulate, const void* dy, const void* a,
                                    const int32_t* counts, void* dW, cudaStream_t s);
 int experts_tc_status_read(int reset);
-moe_status_t launch_weight_grad_simt(int rows, int E, int M, int N, moe_dtype_t dt,
-                                     moe_dtype_t out_dt, int accumulate, const void* dy,
-                                     const void* a, const int32_t* counts, void* dW,
-                                     cudaStream_t s);
+moe_status_t launch_weight_grad_simt(int rows, int E, int M, int N, int accumulate,
+                                     const void* dy, const void* a, const int32_t* counts,
+                                     void* dW, cudaStream_t s);
 
 struct BlockNormArgs {  // pointers of the forward and backward norm and join kernels
   const void *x, *y, *gate, *dres, *dh, *out_in;
