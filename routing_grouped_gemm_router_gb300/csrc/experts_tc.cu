@@ -12,15 +12,29 @@
 // gradients need no transposed copies: a weight read the other way round (down_grad, up_grad) and
 // both operands of the weight gradient are loaded as 64-column boxes, 128 bytes a row, and given
 // to the MMA as M/N-major tiles. Padding each expert's run to 16 rows (one MMA K step) with zeros
-// makes the weight gradient's reduction exact without masks, and lets every 16-row box of an
-// output belong to one expert, so results leave through the TMA: registers -> a swizzled 4 KB
-// tile a warp -> cp.async.bulk.tensor store, full 128-byte lines, ragged edges clipped by the map.
+// makes the weight gradient's reduction exact without masks.
 //
-// Roles in each CTA of a pair: warp 0 issues the TMA loads into a ring of 32 KB stages, warp 1 of
-// the leader issues the MMAs, warps 2-5 are the epilogue over double-buffered accumulators. Work
-// items are (expert, 256-row or 256-column tile, 256-column tile), weight panels outermost within
-// an expert, so that pairs running together share them in L2; persistent CTA pairs take them in
-// turn. All waits are bounded (status kStatusTimeout, no trap).
+// Shared memory is what bounds the products: per MMA an SM reads 8 KB of operands from it in 128
+// clocks at the full tensor rate, while the TMA writes 64 bytes a clock into it (48 with wide items,
+// below), of 128 bytes a clock in all. So the epilogue keeps out of it: a thread holds one row of a
+// tile and stores (and, in down_grad, loads) whole 32-byte sectors of it directly. Measured with
+// 1024 rows an expert, tiles staged through shared memory for full lines took 5 % longer with wide
+// items on and off, whether the TMA or the threads stored them.
+//
+// Roles in each CTA of a pair: warp 0 issues the TMA loads into a ring of stages, warp 1 of the
+// leader issues the MMAs, the others are the epilogue. Tensor memory holds two 256-column
+// accumulators. Work items are (expert, 256-row tile, NH 256-column tiles), weight panels outermost
+// within an expert, so that pairs running together share them in L2; persistent CTA pairs take them
+// in turn. All waits are bounded (status kStatusTimeout, no trap).
+//
+// NH = 2: both accumulators belong to one item, which reads each A tile once for 512 columns, a
+// quarter fewer operand bytes a product; those bytes, not the MMAs, bound the NH = 1 form (with
+// operands of zeros, where power does not count, it ran at 0.67 of the tensor rate whether the ring
+// had 4, 5 or 6 stages). The accumulators are not double-buffered then, so the order of the MMAs hides
+// the epilogue: the first accumulator gets the last stages of an item first, and is drained while
+// the second gets them; an item's first stages go to the first accumulator while the second is
+// still being drained. NH = 1 (the accumulators alternate between items) takes over where the wide
+// items would leave pairs without work.
 #include "tc_ptx.cuh"
 #include "train.cuh"
 
@@ -33,32 +47,29 @@ __device__ int g_status;
 
 enum Kind { kKUp = 0, kKDown = 1, kKDownGrad = 2, kKUpGrad = 3, kKWeight32 = 4, kKWeight16 = 5 };
 
-constexpr int kStages = 5;
-constexpr int kAccs = 2;
 constexpr int kTmemCols = 512;
-constexpr int kThreads = 192;
 constexpr int A_BYTES = 128 * 128;
-constexpr int B_BYTES = 128 * 128;
-constexpr int CHUNK = 64 * 128;    // one 64-column box of an M/N-major operand: 64 K rows x 128 B
-constexpr int OUT_BYTES = 32 * 128;  // one staged output tile of a warp
-constexpr int kOutBufs = 3;        // a warp's tiles: written, being read by the TMA, free
+constexpr int B_BYTES = 128 * 128;   // of one 256-column tile
+constexpr int CHUNK = 64 * 128;      // one 64-column box of an M/N-major operand: 64 K rows x 128 B
 
 template <int KIND>
 struct Traits {
   static constexpr bool weight = KIND >= kKWeight32;
   static constexpr bool a_mn = weight;  // operand contiguous along M rather than K
   static constexpr bool b_mn = KIND >= kKDownGrad;
-  // columns of the result an item covers
-  static constexpr int cols = KIND == kKUp ? 128 : 256;
   static constexpr uint32_t idesc =
       idesc_bf16(256, 256) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
 };
 
+template <int KIND, int NH>
 struct Layout {
+  static constexpr int kStages = NH == 2 ? 4 : 6;
+  static constexpr int kEpiWarps = 8;  // two a 32-lane quarter of tensor memory
+  static constexpr int kThreads = 64 + 32 * kEpiWarps;
+  static constexpr int kStageB = NH * B_BYTES;
   static constexpr size_t a = 0;
   static constexpr size_t b = a + (size_t)kStages * A_BYTES;
-  static constexpr size_t out = b + (size_t)kStages * B_BYTES;
-  static constexpr size_t bars = out + (size_t)4 * kOutBufs * OUT_BYTES;
+  static constexpr size_t bars = b + (size_t)kStages * kStageB;
   static constexpr size_t misc = bars + (2 * kStages + 5) * 8;
   static constexpr size_t start = misc + 16;
   static constexpr size_t cnt = start + (kMaxExperts + 1) * 4;
@@ -66,24 +77,26 @@ struct Layout {
   static constexpr size_t end = pre + (kMaxExperts + 1) * 4;
   static constexpr size_t bytes = 1024 + end;
 };
-static_assert(Layout::bytes <= 232448, "shared memory");
+static_assert(Layout<kKUp, 1>::bytes <= 232448 && Layout<kKUp, 2>::bytes <= 232448, "shared memory");
 
 struct Params {
   const int32_t* counts;
   const float* h13;  // down_grad: the pre-activations [rows, 2I]
-  void* out;         // zeroed tail rows: rows of out_bytes each
-  void* act;         // and of act_bytes each (up, down_grad)
+  void* out;
+  void* act;         // up, down_grad
   int E, rows;
   int M;             // weight: rows of dW[e]
   int N;             // columns of the result (up: I)
   int K;             // reduction (rows kinds)
-  int m_tiles, n_tiles;
+  int m_tiles, n_tiles;  // n_tiles: 256-column tiles (up: 128 gate and up columns)
+  int n_items;           // column items: NH tiles each
   int accumulate;
-  int out_bytes, act_bytes;
+  int out_bytes, act_bytes;  // bytes of a row of out and act
+  int wide;                  // whether all of their rows start on 32-byte boundaries
 };
 
 struct Maps {
-  CUtensorMap a, b0, b1, o0, o1, o2;
+  CUtensorMap a, b0, b1;
 };
 
 // M/N-major operand tile: 128-byte swizzled rows of 64 elements along M or N, one row a K index;
@@ -98,76 +111,86 @@ __device__ __forceinline__ uint64_t mn_desc(uint32_t saddr) {
   return d;
 }
 
-__device__ __forceinline__ void store_2d(const CUtensorMap* tm, const void* src, int c0, int c1) {
-  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
-                   (uint64_t)tm),
-               "r"(c0), "r"(c1), "r"(su32(src))
-               : "memory");
-}
-__device__ __forceinline__ void store_3d(const CUtensorMap* tm, const void* src, int c0, int c1,
-                                         int c2) {
+// Whether a phase has completed, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t* b, uint32_t parity) {
+  uint32_t ok;
   asm volatile(
-      "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
-          (uint64_t)tm),
-      "r"(c0), "r"(c1), "r"(c2), "r"(su32(src))
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(su32(b)), "r"(parity)
       : "memory");
-}
-__device__ __forceinline__ void add_3d(const CUtensorMap* tm, const void* src, int c0, int c1,
-                                       int c2) {
-  asm volatile(
-      "cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], "
-      "[%4];" ::"l"((uint64_t)tm),
-      "r"(c0), "r"(c1), "r"(c2), "r"(su32(src))
-      : "memory");
-}
-__device__ __forceinline__ void store_commit() {
-  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-}
-template <int N>
-__device__ __forceinline__ void store_wait_read() {  // all but the N latest groups have been read
-  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+  return ok != 0;
 }
 
-// The 16-byte piece c of row r of a staged tile (128-byte swizzle, as the output map has it).
-__device__ __forceinline__ uint4* piece(uint8_t* tile, int r, int c) {
-  return reinterpret_cast<uint4*>(tile + r * 128 + ((c ^ (r & 7)) << 4));
+// Thirty-two bytes of a row, to or from global memory: one instruction where `wide` (every row of the
+// matrix starts on a 32-byte boundary), else two. n: 16-byte pieces left of the row's end.
+__device__ __forceinline__ void put32(void* p, const uint32_t (&v)[8], bool wide, int n) {
+  if (wide) {
+    if (n > 0)
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]),
+                   "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                   : "memory");
+  } else {
+    if (n > 0) ((uint4*)p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    if (n > 1) ((uint4*)p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
 }
-// Thirty-two fp32 values of row r: a whole row of an fp32 tile.
-__device__ __forceinline__ void stage_f32(uint8_t* tile, int r, const uint32_t (&v)[32], bool keep) {
+__device__ __forceinline__ void get32(const void* p, uint32_t (&v)[8], bool wide, int n) {
 #pragma unroll
-  for (int c = 0; c < 8; ++c)
-    *piece(tile, r, c) = keep ? make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3])
-                              : make_uint4(0, 0, 0, 0);
+  for (int i = 0; i < 8; ++i) v[i] = 0;
+  if (wide) {
+    if (n > 0)
+      asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                   : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]),
+                     "=r"(v[6]), "=r"(v[7])
+                   : "l"(p)
+                   : "memory");
+  } else {
+    if (n > 0) {
+      const uint4 x = ((const uint4*)p)[0];
+      v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+    }
+    if (n > 1) {
+      const uint4 x = ((const uint4*)p)[1];
+      v[4] = x.x; v[5] = x.y; v[6] = x.z; v[7] = x.w;
+    }
+  }
 }
-// Thirty-two values as bf16: the `half`-th 64 bytes of a row of a bf16 tile.
-__device__ __forceinline__ void stage_bf16(uint8_t* tile, int r, int half, const float (&v)[32],
-                                           bool keep) {
+// Sixteen fp32 values of a row, or thirty-two bf16 ones as pairs: two 32-byte pieces at p.
+__device__ __forceinline__ void put64(void* p, const uint32_t* v, bool wide, int n) {
 #pragma unroll
-  for (int c = 0; c < 4; ++c)
-    *piece(tile, r, half * 4 + c) =
-        keep ? make_uint4(pack_bf16(v[8 * c], v[8 * c + 1]), pack_bf16(v[8 * c + 2], v[8 * c + 3]),
-                          pack_bf16(v[8 * c + 4], v[8 * c + 5]), pack_bf16(v[8 * c + 6], v[8 * c + 7]))
-             : make_uint4(0, 0, 0, 0);
+  for (int h = 0; h < 2; ++h) {
+    uint32_t x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = v[8 * h + i];
+    put32((uint8_t*)p + 32 * h, x, wide, n - 2 * h);
+  }
 }
+
+// The hardware's exponential and reciprocal, each off by a few units of fp32's last place: results
+// are rounded to bf16, and the epilogue has to keep up with the tensor cores.
+__device__ __forceinline__ float sigmoid(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
 
 struct Item {
-  int e, n;        // expert, column tile
+  int e, n, nh;    // expert, first column tile, column tiles
   int m0;          // first row of the tile (weight: first row of dW[e])
   int row0, cnt;   // the expert's rows
   int num_kb;
   bool live1;      // the peer's half of the tile holds rows
 };
 
-template <int KIND>
+template <int KIND, int NH>
 __device__ __forceinline__ Item item_of(int w, const Params& P, const int* start, const int* cnt,
                                         const int* pre) {
   Item it;
+  int n;
   if (Traits<KIND>::weight) {
-    const int per = P.m_tiles * P.n_tiles;
+    const int per = P.m_tiles * P.n_items;
     it.e = w / per;
     const int rest = w - it.e * per;
-    it.n = rest % P.n_tiles;
-    it.m0 = rest / P.n_tiles * 256;
+    n = rest % P.n_items;
+    it.m0 = rest / P.n_items * 256;
     it.row0 = start[it.e];
     it.cnt = cnt[it.e];
     it.num_kb = (it.cnt + BK - 1) / BK;
@@ -176,40 +199,44 @@ __device__ __forceinline__ Item item_of(int w, const Params& P, const int* start
     int lo = 0, hi = P.E - 1;  // the last expert whose first item is at or before w
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (pre[mid] * P.n_tiles <= w) lo = mid; else hi = mid - 1;
+      if (pre[mid] * P.n_items <= w) lo = mid; else hi = mid - 1;
     }
     const int c = pre[lo + 1] - pre[lo];
-    const int local = w - pre[lo] * P.n_tiles;
+    const int local = w - pre[lo] * P.n_items;
     it.e = lo;
-    it.n = local / c;
-    const int i = local - it.n * c;
+    n = local / c;
+    const int i = local - n * c;
     it.row0 = start[lo];
     it.cnt = cnt[lo];
     it.m0 = it.row0 + i * 256;
     it.num_kb = (P.K + BK - 1) / BK;
     it.live1 = i * 256 + 128 < it.cnt;
   }
+  it.n = n * NH;
+  it.nh = min(NH, P.n_tiles - it.n);
   return it;
 }
 
-template <int KIND>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+template <int KIND, int NH>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<KIND, NH>::kThreads, 1)
     expert_pair_kernel(const __grid_constant__ Maps TM, const Params P) {
   using R = Traits<KIND>;
+  using LY = Layout<KIND, NH>;
+  constexpr int kStages = LY::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  uint8_t* sA = smem + Layout::a;
-  uint8_t* sB = smem + Layout::b;
-  uint64_t* full = (uint64_t*)(smem + Layout::bars);
+  uint8_t* sA = smem + LY::a;
+  uint8_t* sB = smem + LY::b;
+  uint64_t* full = (uint64_t*)(smem + LY::bars);
   uint64_t* empty = full + kStages;
-  uint64_t* tfull = empty + kStages;
+  uint64_t* tfull = empty + kStages;  // per accumulator
   uint64_t* tempty = tfull + 2;
   uint64_t* drain = tempty + 2;
-  uint32_t* tmem_slot = (uint32_t*)(smem + Layout::misc);
-  volatile int* abort_flag = (volatile int*)(smem + Layout::misc + 4);
-  int* start = (int*)(smem + Layout::start);
-  int* cnt = (int*)(smem + Layout::cnt);
-  int* pre = (int*)(smem + Layout::pre);
+  uint32_t* tmem_slot = (uint32_t*)(smem + LY::misc);
+  volatile int* abort_flag = (volatile int*)(smem + LY::misc + 4);
+  int* start = (int*)(smem + LY::start);
+  int* cnt = (int*)(smem + LY::cnt);
+  int* pre = (int*)(smem + LY::pre);
   int* status = &g_status;
 
   pdl_trigger();
@@ -224,14 +251,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
-      mbar_init(&tempty[b], 8);  // four epilogue warps of each CTA (the leader's is used)
+      mbar_init(&tempty[b], 2 * LY::kEpiWarps);  // both CTAs' epilogue warps (the leader's is used)
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
     mbar_init_fence();
     prefetch_tmap(&TM.a);
     prefetch_tmap(&TM.b0);
-    prefetch_tmap(&TM.o0);
   }
   if (warp == 1) {
     tmem_alloc<2>(tmem_slot, kTmemCols);
@@ -277,45 +303,55 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   }
   __syncthreads();
-  const int total = R::weight ? P.E * P.m_tiles * P.n_tiles : pre[P.E] * P.n_tiles;
+  const int total = R::weight ? P.E * P.m_tiles * P.n_items : pre[P.E] * P.n_items;
   const int pair = blockIdx.x >> 1, num_pairs = gridDim.x >> 1;
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
-      int g = 0;
+      int s = 0;
+      uint32_t phase = 0;
       bool ok = true;
       for (int w = pair; w < total && ok; w += num_pairs) {
-        const Item it = item_of<KIND>(w, P, start, cnt, pre);
-        for (int kb = 0; kb < it.num_kb; ++kb, ++g) {
-          const int s = g % kStages;
-          if (!wait_bounded(&empty[s], ((uint32_t)(g / kStages) & 1u) ^ 1u, abort_flag, status)) {
+        const Item it = item_of<KIND, NH>(w, P, start, cnt, pre);
+        const uint32_t bytes = 2u * (A_BYTES + it.nh * B_BYTES) - (it.live1 ? 0u : (uint32_t)A_BYTES);
+        for (int kb = 0; kb < it.num_kb; ++kb) {
+          if (!wait_bounded(&empty[s], phase ^ 1u, abort_flag, status)) {
             ok = false;
             break;
           }
           const uint32_t fl = cluster_addr(&full[s], 0);
-          if (leader)
-            mbar_expect_tx(&full[s], 2u * (A_BYTES + B_BYTES) - (it.live1 ? 0u : (uint32_t)A_BYTES));
+          if (leader) mbar_expect_tx(&full[s], bytes);
           uint8_t* a = sA + s * A_BYTES;
-          uint8_t* b = sB + s * B_BYTES;
+          uint8_t* b = sB + s * LY::kStageB;
           if (R::weight) {
-            const int y = it.row0 + kb * BK, m = it.m0 + (int)rank * 128, n = it.n * 256 + (int)rank * 128;
+            const int y = it.row0 + kb * BK, m = it.m0 + (int)rank * 128;
             tma_2d_pair(a, &TM.a, fl, m, y);
             tma_2d_pair(a + CHUNK, &TM.a, fl, m + 64, y);
-            tma_2d_pair(b, &TM.b0, fl, n, y);
-            tma_2d_pair(b + CHUNK, &TM.b0, fl, n + 64, y);
+            for (int h = 0; h < it.nh; ++h, b += B_BYTES) {
+              const int n = (it.n + h) * 256 + (int)rank * 128;
+              tma_2d_pair(b, &TM.b0, fl, n, y);
+              tma_2d_pair(b + CHUNK, &TM.b0, fl, n + 64, y);
+            }
           } else {
             // the peer's rows of a half-filled tile are neither loaded nor stored
             if (leader || it.live1) tma_2d_pair(a, &TM.a, fl, kb * BK, it.m0 + (int)rank * 128);
-            if (KIND == kKUp) {  // leader: gate rows, peer: the same up rows
-              tma_3d_pair(b, rank ? &TM.b1 : &TM.b0, fl, kb * BK, it.n * 128, it.e);
-            } else if (KIND == kKDown) {
-              tma_3d_pair(b, &TM.b0, fl, kb * BK, it.n * 256 + (int)rank * 128, it.e);
-            } else {
-              const int n = it.n * 256 + (int)rank * 128;
-              tma_3d_pair(b, &TM.b0, fl, n, kb * BK, it.e);
-              tma_3d_pair(b + CHUNK, &TM.b0, fl, n + 64, kb * BK, it.e);
+            for (int h = 0; h < it.nh; ++h, b += B_BYTES) {
+              const int n = it.n + h;
+              if (KIND == kKUp) {  // leader: gate rows, peer: the same up rows
+                tma_3d_pair(b, rank ? &TM.b1 : &TM.b0, fl, kb * BK, n * 128, it.e);
+              } else if (KIND == kKDown) {
+                tma_3d_pair(b, &TM.b0, fl, kb * BK, n * 256 + (int)rank * 128, it.e);
+              } else {
+                const int c = n * 256 + (int)rank * 128;
+                tma_3d_pair(b, &TM.b0, fl, c, kb * BK, it.e);
+                tma_3d_pair(b + CHUNK, &TM.b0, fl, c + 64, kb * BK, it.e);
+              }
             }
+          }
+          if (++s == kStages) {
+            s = 0;
+            phase ^= 1u;
           }
         }
       }
@@ -324,39 +360,95 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------ leader: MMA issuer
     if (leader && lane == 0) {
-      int g = 0, acc = 0;
+      // stages are counted: stage number g sits in slot g % kStages; acc_phase bit a is the phase
+      // of accumulator a
+      int g0 = 0, acc = 0;
       uint32_t acc_phase = 0;
-      bool ok = true, issued = false;
+      bool issued = false, ok = true;
       for (int w = pair; w < total && ok; w += num_pairs) {
-        const Item it = item_of<KIND>(w, P, start, cnt, pre);
-        if (it.num_kb == 0) continue;
-        if (!wait_bounded(&tempty[acc], acc_phase ^ 1u, abort_flag, status)) break;
-        tc_fence_after();
-        if (*abort_flag) break;
-        const uint32_t d = tmem_base + (uint32_t)(acc * 256);
+        const Item it = item_of<KIND, NH>(w, P, start, cnt, pre);
+        const int T = it.num_kb;
+        if (T == 0) continue;
         const int K = R::weight ? it.cnt : P.K;
-        for (int kb = 0; kb < it.num_kb; ++kb, ++g) {
-          const int s = g % kStages;
-          if (!wait_bounded(&full[s], (uint32_t)(g / kStages) & 1u, abort_flag, status)) {
-            ok = false;
-            break;
-          }
+        auto wait_full = [&](int kb) {
+          const int g = g0 + kb;
+          if (!wait_bounded(&full[g % kStages], (uint32_t)(g / kStages) & 1u, abort_flag, status))
+            return false;
           tc_fence_after();
-          const uint32_t a = su32(sA + s * A_BYTES), b = su32(sB + s * B_BYTES);
+          return true;
+        };
+        // stage kb into accumulator a, B tile h
+        auto mma = [&](int kb, int h, int a) {
+          const int s = (g0 + kb) % kStages;
+          const uint32_t sa = su32(sA + s * A_BYTES), sb = su32(sB + s * LY::kStageB + h * B_BYTES);
+          const uint32_t d = tmem_base + (uint32_t)(a * 256);
           const int steps = min(BK / UMMA_K, (K - kb * BK + UMMA_K - 1) / UMMA_K);
 #pragma unroll
           for (int kk = 0; kk < BK / UMMA_K; ++kk) {
             if (kk < steps)
-              umma_bf16<2>(d, R::a_mn ? mn_desc(a + kk * 2048) : sw128_desc(a + kk * 32),
-                           R::b_mn ? mn_desc(b + kk * 2048) : sw128_desc(b + kk * 32), R::idesc,
+              umma_bf16<2>(d, R::a_mn ? mn_desc(sa + kk * 2048) : sw128_desc(sa + kk * 32),
+                           R::b_mn ? mn_desc(sb + kk * 2048) : sw128_desc(sb + kk * 32), R::idesc,
                            (kb | kk) != 0 ? 1u : 0u);
           }
-          umma_commit_pair(&empty[s], 0x3);
           issued = true;
+        };
+        auto release = [&](int kb) { umma_commit_pair(&empty[(g0 + kb) % kStages], 0x3); };
+        auto acc_free = [&](int a) {
+          if (!wait_bounded(&tempty[a], ((acc_phase >> a) & 1u) ^ 1u, abort_flag, status)) return false;
+          tc_fence_after();
+          return *abort_flag == 0;
+        };
+        if (NH == 1 || it.nh == 1) {
+          const int a = NH == 1 ? acc : 0;
+          if (!acc_free(a)) break;
+          for (int kb = 0; kb < T && ok; ++kb) {
+            if (!(ok = wait_full(kb))) break;
+            mma(kb, 0, a);
+            release(kb);
+          }
+          if (!ok) break;
+          umma_commit_pair(&tfull[a], 0x3);
+          acc_phase ^= 1u << a;
+          if (NH == 1) acc ^= 1;
+        } else {
+          if (!acc_free(0)) break;
+          // the first stages for accumulator 0 alone, while 1 is still being drained
+          int p = 0;
+          while (p < min(kStages, T) && ok && !mbar_test(&tempty[1], ((acc_phase >> 1) & 1u) ^ 1u)) {
+            if (!(ok = wait_full(p))) break;
+            mma(p++, 0, 0);
+          }
+          if (!ok || !acc_free(1)) break;
+          if (p == T) umma_commit_pair(&tfull[0], 0x3);
+          int r = 0;
+          for (; r < p; ++r) {
+            mma(r, 1, 1);
+            release(r);
+          }
+          for (; p < T - kStages && ok; ++p, ++r) {
+            if (!(ok = wait_full(p))) break;
+            mma(p, 0, 0);
+            mma(p, 1, 1);
+            release(p);
+          }
+          if (!ok) break;
+          // the last stages: all of them for accumulator 0, which its epilogue then drains
+          if (p < T) {
+            for (; p < T && ok; ++p) {
+              if (!(ok = wait_full(p))) break;
+              mma(p, 0, 0);
+            }
+            if (!ok) break;
+            umma_commit_pair(&tfull[0], 0x3);
+            for (; r < T; ++r) {
+              mma(r, 1, 1);
+              release(r);
+            }
+          }
+          umma_commit_pair(&tfull[1], 0x3);
+          acc_phase ^= 3u;
         }
-        if (!ok) break;
-        umma_commit_pair(&tfull[acc], 0x3);
-        if (++acc == kAccs) { acc = 0; acc_phase ^= 1u; }
+        g0 += T;
       }
       if (issued) {  // every MMA of this thread finished before tensor memory is freed
         umma_commit<2>(drain);
@@ -365,220 +457,195 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else {
-    // ------------------------------------------------------------ epilogue (4 warps)
-    const int q = warp & 3;  // tensor-memory lanes q*32 .. q*32+31
-    uint8_t* tiles = smem + Layout::out + (size_t)(warp - 2) * kOutBufs * OUT_BYTES;
-    int buf = 0;
+    // ------------------------------------------------------------ epilogue
+    const int q = warp & 3;                 // tensor-memory lanes q*32 .. q*32+31
+    const int part = (warp - 2) >> 2;       // which half of a tile's columns
+    constexpr int kCols = 256 / (LY::kEpiWarps / 4);
     if (!R::weight) {  // rows past the last run are zeroed while the first tile is computed
       const int t = (warp - 2) * 32 + lane;
       const uint4 z = make_uint4(0, 0, 0, 0);
       for (int p = start[P.E] + (int)blockIdx.x; p < P.rows; p += gridDim.x) {
-        for (int v = t; v < P.out_bytes / 16; v += 128)
+        for (int v = t; v < P.out_bytes / 16; v += 32 * LY::kEpiWarps)
           ((uint4*)((uint8_t*)P.out + (int64_t)p * P.out_bytes))[v] = z;
-        for (int v = t; v < P.act_bytes / 16; v += 128)
+        for (int v = t; v < P.act_bytes / 16; v += 32 * LY::kEpiWarps)
           ((uint4*)((uint8_t*)P.act + (int64_t)p * P.act_bytes))[v] = z;
       }
     }
-    // the next staged tile, once the TMA has read what it held three stores ago
-    auto next_tile = [&]() {
-      if (lane == 0) store_wait_read<kOutBufs - 1>();
-      __syncwarp();
-      uint8_t* t = tiles + buf * OUT_BYTES;
-      buf = buf + 1 == kOutBufs ? 0 : buf + 1;
-      return t;
-    };
     int acc = 0;
     uint32_t acc_phase = 0;
-    for (int w = pair; w < total; w += num_pairs) {
-      const Item it = item_of<KIND>(w, P, start, cnt, pre);
+    bool ok_all = true;
+    for (int w = pair; w < total && ok_all; w += num_pairs) {
+      const Item it = item_of<KIND, NH>(w, P, start, cnt, pre);
       if (R::weight && it.num_kb == 0 && P.accumulate) continue;
       const bool computed = it.num_kb != 0;
-      if (computed) {
-        int ok = 1;
-        if (lane == 0) ok = wait_bounded(&tfull[acc], acc_phase, abort_flag, status);
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok) break;
-        tc_fence_after();
-      }
-      const uint32_t tb = tmem_base + (uint32_t)(acc * 256) + ((uint32_t)(q * 32) << 16);
       const int m = it.m0 + (int)rank * 128 + q * 32;  // first row of this warp's 32
-      auto load = [&](uint32_t (&v)[32], int col) {
-        tmem_ld32(tb + col, v);
-        tmem_ld_wait();
-      };
-      if (R::weight) {
-        // dW[e][m .. m+31][...]: whole 32-row boxes, edges clipped by the map
-        constexpr int W = KIND == kKWeight32 ? 32 : 64;
-        const int n0 = it.n * 256;
-#pragma unroll 1
-        for (int c = 0; c < 256; c += W) {
-          if (n0 + c >= P.N || m >= P.M) break;
-          uint8_t* t = next_tile();
-          if (KIND == kKWeight32) {
-            uint32_t v[32];
-            if (computed) load(v, c);
-            stage_f32(t, lane, v, computed);
-          } else {
+      // this thread's row: whether it is stored (rows kinds: up to the run's padded end, zeros past cnt)
+      const int end = R::weight ? P.M : min(it.row0 + (it.cnt + kRowBlock - 1) / kRowBlock * kRowBlock, P.rows);
+      const bool store = m + lane < end;
+      const bool slot = R::weight ? computed : m + lane < it.row0 + it.cnt;
+      uint8_t* const out = (uint8_t*)P.out + ((R::weight ? (int64_t)it.e * P.M : 0) + m + lane) * P.out_bytes;
+      uint8_t* const act = (uint8_t*)P.act + (int64_t)(m + lane) * P.act_bytes;
+      const float* const hrow = P.h13 + (int64_t)(m + lane) * 2 * P.N;
+      const bool wide = P.wide;
+      for (int h = 0; h < it.nh; ++h) {
+        const int a = NH == 1 ? acc : h;
+        const int n = it.n + h;
+        // 16-byte pieces of a row of es-byte values that lie left of column N
+        auto left = [&](int col, int es) { return (P.N - col) * es / 16; };
+        uint32_t gq[4][8], uq[4][8];  // down_grad: pre-activations, asked for before they are needed
+        auto ask = [&](int col) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint32_t v[32];
-              float f[32];
-              if (computed) load(v, c + 32 * h);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]);
-              if (P.accumulate && m + lane < P.M) {  // one rounding of the sum
-                const __nv_bfloat16* old = (const __nv_bfloat16*)P.out +
-                                           ((int64_t)it.e * P.M + m + lane) * P.N + n0 + c + 32 * h;
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  if (n0 + c + 32 * h + 8 * i < P.N) {
-                    float o[8];
-                    Vec<__nv_bfloat16>::unpack(((const uint4*)old)[i], o);
-#pragma unroll
-                    for (int x = 0; x < 8; ++x) f[8 * i + x] += o[x];
-                  }
-              }
-              stage_bf16(t, lane, h, f, computed);
-            }
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            if (KIND == kKWeight32 && P.accumulate) add_3d(&TM.o0, t, n0 + c, m, it.e);
-            else store_3d(&TM.o0, t, n0 + c, m, it.e);
-            store_commit();
-          }
-        }
-      } else {
-        // 16-row boxes up to the run's padded end; rows past cnt are stored as zeros
-        const int end = min(it.row0 + (it.cnt + kRowBlock - 1) / kRowBlock * kRowBlock, P.rows);
-        const bool slot = m + lane < it.row0 + it.cnt;
-        // one group a tile, empty where nothing is stored: next_tile counts groups
-        auto put = [&](const CUtensorMap* tm, uint8_t* t, int col) {
-          if (lane == 0) {
-            if (col < P.N && m < end) store_2d(tm, t, col, m);
-            if (col < P.N && m + 16 < end) store_2d(tm, t + 16 * 128, col, m + 16);
-            store_commit();
+          for (int i = 0; i < 4; ++i) {
+            const int k = slot ? left(col + 8 * i, 4) : 0;
+            get32(hrow + col + 8 * i, gq[i], wide, k);
+            get32(hrow + P.N + col + 8 * i, uq[i], wide, k);
           }
         };
-        if (KIND == kKUp) {
-          const int n0 = it.n * 128;
+        if (KIND == kKDownGrad) ask(n * 256 + part * kCols);
+        if (computed) {
+          int ok = 1;
+          if (lane == 0) ok = wait_bounded(&tfull[a], (acc_phase >> a) & 1u, abort_flag, status);
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          if (!ok) {
+            ok_all = false;
+            break;
+          }
+          tc_fence_after();
+        }
+        const uint32_t tb = tmem_base + (uint32_t)(a * 256) + ((uint32_t)(q * 32) << 16);
+        const bool some = m < end;  // of the warp
+        if (some && KIND == kKUp) {
+          const int n0 = n * 128;
 #pragma unroll 1
-          for (int c = 0; c < 128 && m < end; c += 64) {
-            if (n0 + c >= P.N) break;
-            uint32_t ap[32];  // the 64 activations as bf16 pairs
+          for (int c = part * (kCols / 2); c < (part + 1) * (kCols / 2); c += 32) {
+            const int col = n0 + c;
+            if (col >= P.N) break;
+            __syncwarp();
+            uint32_t g32[32], u32[32], ap[16];
+            tmem_ld32(tb + c, g32);
+            tmem_ld32(tb + 128 + c, u32);
+            tmem_ld_wait();
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint32_t gv[32], uv[32];
-              tmem_ld32(tb + c + 32 * h, gv);
-              tmem_ld32(tb + 128 + c + 32 * h, uv);
+            for (int i = 0; i < 16; ++i) {
+              float a2[2];
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                const int j = 2 * i + y;
+                if (!slot) g32[j] = u32[j] = 0;
+                const float g = __uint_as_float(g32[j]);
+                a2[y] = g * sigmoid(g) * __uint_as_float(u32[j]);
+              }
+              ap[i] = pack_bf16(a2[0], a2[1]);
+            }
+            if (store) {
+              const int k = left(col, 4);
+              put64(out + (int64_t)col * 4, g32, wide, k);
+              put64(out + (int64_t)col * 4 + 64, g32 + 16, wide, k - 4);
+              put64(out + ((int64_t)P.N + col) * 4, u32, wide, k);
+              put64(out + ((int64_t)P.N + col) * 4 + 64, u32 + 16, wide, k - 4);
+              put64(act + (int64_t)col * 2, ap, wide, left(col, 2));
+            }
+          }
+        } else if (some && KIND == kKDownGrad) {
+          const int n0 = n * 256;
+#pragma unroll 1
+          for (int c = part * kCols; c < (part + 1) * kCols; c += 32) {
+            const int col = n0 + c;
+            if (col >= P.N) break;
+            __syncwarp();
+            uint32_t dv[32], dg[16], du[16], ap[16];
+            tmem_ld32(tb + c, dv);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              float x[2], y[2], z[2];
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const int j = 2 * i + k;
+                const float d = __uint_as_float(dv[j]), g = __uint_as_float(gq[j / 8][j % 8]);
+                const float u = __uint_as_float(uq[j / 8][j % 8]), s = sigmoid(g);
+                x[k] = d * u * s * (1.f + g * (1.f - s));
+                y[k] = d * g * s;
+                z[k] = g * s * u;
+              }
+              dg[i] = slot ? pack_bf16(x[0], x[1]) : 0u;
+              du[i] = slot ? pack_bf16(y[0], y[1]) : 0u;
+              ap[i] = slot ? pack_bf16(z[0], z[1]) : 0u;
+            }
+            if (c + 32 < (part + 1) * kCols) ask(col + 32);  // on their way during what follows
+            if (store) {
+              const int k = left(col, 2);
+              put64(out + (int64_t)col * 2, dg, wide, k);
+              put64(out + ((int64_t)P.N + col) * 2, du, wide, k);
+              put64(act + (int64_t)col * 2, ap, wide, k);
+            }
+          }
+        } else if (some) {  // down, up_grad, dW
+          const int n0 = n * 256;
+#pragma unroll 1
+          for (int c = part * kCols; c < (part + 1) * kCols; c += 32) {
+            const int col = n0 + c;
+            if (col >= P.N) break;
+            __syncwarp();
+            uint32_t v[32];
+            if (computed) {
+              tmem_ld32(tb + c, v);
               tmem_ld_wait();
-              uint8_t* tg = next_tile();
-              stage_f32(tg, lane, gv, slot);
-              fence_proxy_async_smem();
-              __syncwarp();
-              put(&TM.o0, tg, n0 + c + 32 * h);
-              uint8_t* tu = next_tile();
-              stage_f32(tu, lane, uv, slot);
-              fence_proxy_async_smem();
-              __syncwarp();
-              put(&TM.o1, tu, n0 + c + 32 * h);
+            }
+            if (!slot) {
 #pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                float a2[2];
+              for (int i = 0; i < 32; ++i) v[i] = 0;
+            }
+            if (!store) {
+            } else if (KIND == kKWeight32) {
+              const int k = left(col, 4);
+              if (P.accumulate) {
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                  const float g = __uint_as_float(gv[2 * i + x]);
-                  a2[x] = g * (1.f / (1.f + expf(-g))) * __uint_as_float(uv[2 * i + x]);
+                for (int i = 0; i < 4; ++i) {
+                  uint32_t o[8];
+                  get32(out + (int64_t)col * 4 + 32 * i, o, wide, k - 2 * i);
+#pragma unroll
+                  for (int j = 0; j < 8; ++j)
+                    v[8 * i + j] = __float_as_uint(__uint_as_float(v[8 * i + j]) + __uint_as_float(o[j]));
                 }
-                ap[16 * h + i] = slot ? pack_bf16(a2[0], a2[1]) : 0u;
               }
-            }
-            uint8_t* ta = next_tile();
+              put64(out + (int64_t)col * 4, v, wide, k);
+              put64(out + (int64_t)col * 4 + 64, v + 16, wide, k - 4);
+            } else {
+              const int k = left(col, 2);
+              if (R::weight && P.accumulate) {  // one rounding of the sum
 #pragma unroll
-            for (int p = 0; p < 8; ++p)
-              *piece(ta, lane, p) = make_uint4(ap[4 * p], ap[4 * p + 1], ap[4 * p + 2], ap[4 * p + 3]);
-            fence_proxy_async_smem();
-            __syncwarp();
-            put(&TM.o2, ta, n0 + c);
-          }
-        } else if (KIND == kKDownGrad) {
-          const int n0 = it.n * 256;
-          const float* hrow = P.h13 + (int64_t)(m + lane) * 2 * P.N;
-#pragma unroll 1
-          for (int c = 0; c < 256 && m < end; c += 64) {
-            if (n0 + c >= P.N) break;
-            uint8_t *tg = next_tile(), *tu = next_tile(), *ta = next_tile();
-            if (lane == 0) store_wait_read<0>();  // all three are written at once
-            __syncwarp();
-#pragma unroll 1
-            for (int h = 0; h < 2; ++h) {
-              const int col = n0 + c + 32 * h;
-              float gv[32], uv[32];
+                for (int i = 0; i < 2; ++i) {
+                  uint32_t o[8];
+                  get32(out + (int64_t)col * 2 + 32 * i, o, wide, k - 2 * i);
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-                if (slot && col + 4 * i < P.N) {
-                  a = __ldg((const float4*)(hrow + col) + i);
-                  b = __ldg((const float4*)(hrow + P.N + col) + i);
+                  for (int j = 0; j < 8; ++j) {
+                    const int x = 16 * i + 2 * j;
+                    v[x] = __float_as_uint(__uint_as_float(v[x]) + __uint_as_float(o[j] << 16));
+                    v[x + 1] = __float_as_uint(__uint_as_float(v[x + 1]) + __uint_as_float(o[j] & 0xFFFF0000u));
+                  }
                 }
-                gv[4 * i] = a.x; gv[4 * i + 1] = a.y; gv[4 * i + 2] = a.z; gv[4 * i + 3] = a.w;
-                uv[4 * i] = b.x; uv[4 * i + 1] = b.y; uv[4 * i + 2] = b.z; uv[4 * i + 3] = b.w;
               }
-              uint32_t dv[32];
-              load(dv, c + 32 * h);
-              float av[32];
+              uint32_t pr[16];
 #pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                const float d = __uint_as_float(dv[i]), g = gv[i], u = uv[i];
-                const float s = 1.f / (1.f + expf(-g));
-                av[i] = g * s * u;
-                gv[i] = d * u * s * (1.f + g * (1.f - s));
-                uv[i] = d * g * s;
-              }
-              stage_bf16(tg, lane, h, gv, slot);
-              stage_bf16(tu, lane, h, uv, slot);
-              stage_bf16(ta, lane, h, av, slot);
+              for (int i = 0; i < 16; ++i)
+                pr[i] = pack_bf16(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+              put64(out + (int64_t)col * 2, pr, wide, k);
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-            put(&TM.o0, tg, n0 + c);
-            put(&TM.o1, tu, n0 + c);
-            put(&TM.o2, ta, n0 + c);
-          }
-        } else {
-          const int n0 = it.n * 256;
-#pragma unroll 1
-          for (int c = 0; c < 256 && m < end; c += 64) {
-            if (n0 + c >= P.N) break;
-            uint8_t* t = next_tile();
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint32_t v[32];
-              float f[32];
-              load(v, c + 32 * h);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]);
-              stage_bf16(t, lane, h, f, slot);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            put(&TM.o0, t, n0 + c);
           }
         }
-      }
-      if (computed) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          if (leader) mbar_arrive(&tempty[acc]);
-          else mbar_arrive_cta(&tempty[acc], 0);
+        if (computed) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (leader) mbar_arrive(&tempty[a]);
+            else mbar_arrive_cta(&tempty[a], 0);
+          }
+          acc_phase ^= 1u << a;
+          if (NH == 1) acc ^= 1;
         }
-        if (++acc == kAccs) { acc = 0; acc_phase ^= 1u; }
       }
     }
-    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-    __syncwarp();
   }
 
   __syncthreads();
@@ -594,24 +661,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
 }
 
-// Output map: boxes of 128-byte rows, 128-byte swizzle.
-static bool make_out_map(CUtensorMap* m, void* base, bool f32, int rank, const uint64_t* dims,
-                         const uint64_t* strides_elems, uint32_t box_rows) {
-  auto fn = encode_fn();
-  if (!fn) return false;
-  cuuint64_t gdim[3], gstr[2];
-  cuuint32_t bdim[3] = {f32 ? 32u : 64u, box_rows, 1u}, estr[3] = {1, 1, 1};
-  for (int i = 0; i < rank; ++i) gdim[i] = dims[i];
-  for (int i = 0; i + 1 < rank; ++i) gstr[i] = strides_elems[i] * (f32 ? 4 : 2);
-  return fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, base,
-            gdim, gstr, bdim, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-template <int KIND>
-static moe_status_t launch(const Maps& tm, const Params& P, int64_t max_items, cudaStream_t s) {
-  auto kern = expert_pair_kernel<KIND>;
-  constexpr size_t smem = Layout::bytes;
+template <int KIND, int NH>
+static moe_status_t launch(const Maps& tm, Params P, int64_t max_rows_items, int resident_only,
+                           int* resident_out, cudaStream_t s) {
+  auto kern = expert_pair_kernel<KIND, NH>;
+  constexpr size_t smem = Layout<KIND, NH>::bytes;
+  constexpr int threads = Layout<KIND, NH>::kThreads;
   // persistent grid: as many CTA pairs as can be resident at once
   static thread_local int configured_dev = -1, resident = 0;
   int dev = 0;
@@ -622,7 +677,7 @@ static moe_status_t launch(const Maps& tm, const Params& P, int64_t max_items, c
       return MOE_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * (num_sms() / 2));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     int clusters = 0;
     if (cudaOccupancyMaxActiveClusters(&clusters, (void*)kern, &cfg) != cudaSuccess ||
@@ -633,8 +688,49 @@ static moe_status_t launch(const Maps& tm, const Params& P, int64_t max_items, c
     resident = std::min(clusters, num_sms() / 2);
     configured_dev = dev;
   }
-  const int pairs = (int)std::max<int64_t>(1, std::min<int64_t>(resident, max_items));
-  return launch_k(kern, dim3(2 * pairs), dim3(kThreads), smem, s, tm, P);
+  if (resident_only) {
+    *resident_out = resident;
+    return MOE_OK;
+  }
+  P.n_items = ceil_div(P.n_tiles, NH);
+  const int64_t items = max_rows_items * P.n_items;
+  const int pairs = (int)std::max<int64_t>(1, std::min<int64_t>(resident, items));
+  return launch_k(kern, dim3(2 * pairs), dim3(threads), smem, s, tm, P);
+}
+
+// Wide items (NH = 2) take over from this reduction length on (average rows an expert for the weight
+// gradients); below it the epilogue that they leave uncovered costs more than they save. Measured at
+// 8 to 64 experts of 512 to 4096 rows, narrow against wide, us: up 2048 long 419 and 460, 4096 1326
+// and 1290, 8192 1530 and 1392; down 1024 197 and 211, 2048 757 and 720, 14336 687 and 648; up_grad 2048
+// 380 and 361, 4096 390 and 348; bf16 weights over 512 rows 247 and 271, 1024 1381 and 1396, 2048
+// 1510 and 1412; fp32 ones over 2048 rows 393 and 414, 4096 382 and 370. Down_grad, whose epilogue reads
+// the most, lost at every length (8192: 889 against 874 at best, 4096 801 and 935): it has no wide form.
+template <int KIND>
+constexpr int kWideFrom = KIND == kKUp         ? 4096
+                          : KIND == kKDown     ? 2048
+                          : KIND == kKUpGrad   ? 2048
+                          : KIND == kKWeight16 ? 1536
+                          : KIND == kKWeight32 ? 2560
+                                               : 0;
+// And from this many wide items a resident CTA pair on: with fewer, the last round leaves too many
+// pairs without work.
+constexpr int kWideRounds = 3;
+
+// row_items: row tiles that are sure to have work (how they fall on the experts is known on the device
+// only); max_row_items: the most there can be.
+template <int KIND>
+static moe_status_t launch_either(const Maps& tm, const Params& P, int reduction, int64_t row_items,
+                                  int64_t max_row_items, cudaStream_t s) {
+  if (max_row_items * P.n_tiles > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
+  if constexpr (kWideFrom<KIND> > 0) {
+    int resident = 0;
+    const moe_status_t st = launch<KIND, 2>(tm, P, 0, 1, &resident, s);
+    if (st != MOE_OK) return st;
+    if (reduction >= kWideFrom<KIND> &&
+        row_items * ceil_div(P.n_tiles, 2) >= (int64_t)kWideRounds * resident)
+      return launch<KIND, 2>(tm, P, max_row_items, 0, nullptr, s);
+  }
+  return launch<KIND, 1>(tm, P, max_row_items, 0, nullptr, s);
 }
 
 }  // namespace etc
@@ -681,10 +777,6 @@ moe_status_t launch_expert_product_tc(ExpertProduct kind, const moe_experts_t& c
     uint32_t box[3] = {BK, 128, 1};
     ok &= make_map(&tm.b0, w, 3, d, st, box, true);
     ok &= make_map(&tm.b1, (const __nv_bfloat16*)w + I * H, 3, d, st, box, true);
-    uint64_t od[2] = {I, rows}, os[1] = {2 * I}, as[1] = {I};
-    ok &= make_out_map(&tm.o0, out, true, 2, od, os, 16);
-    ok &= make_out_map(&tm.o1, (float*)out + I, true, 2, od, os, 16);
-    ok &= make_out_map(&tm.o2, act, false, 2, od, as, 16);
   } else if (kind == kDown) {
     uint64_t d[3] = {I, H, E}, st[2] = {I, H * I};
     uint32_t box[3] = {BK, 128, 1};
@@ -696,23 +788,14 @@ moe_status_t launch_expert_product_tc(ExpertProduct kind, const moe_experts_t& c
     uint32_t box[3] = {64, BK, 1};
     ok &= make_map(&tm.b0, w, 3, d, st, box, true);
   }
-  if (dgrad) {
-    uint64_t od[2] = {I, rows}, os[1] = {2 * I}, as[1] = {I};
-    ok &= make_out_map(&tm.o0, out, false, 2, od, os, 16);
-    ok &= make_out_map(&tm.o1, (__nv_bfloat16*)out + I, false, 2, od, os, 16);
-    ok &= make_out_map(&tm.o2, act, false, 2, od, as, 16);
-  } else if (!up) {
-    uint64_t od[2] = {H, rows}, os[1] = {H};
-    ok &= make_out_map(&tm.o0, out, false, 2, od, os, 16);
-  }
   if (!ok) return MOE_ERR_CUDA;
-  const int64_t items = ((int64_t)c.rows / 256 + c.E) * P.n_tiles;
-  if (items > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
+  P.wide = (((uintptr_t)out | (uintptr_t)act | (uintptr_t)h13) & 31u) == 0 && P.N % 16 == 0;
+  const int64_t least = ceil_div(c.rows, 256), most = (int64_t)c.rows / 256 + c.E;
   switch (kind) {
-    case kUp: return launch<kKUp>(tm, P, items, s);
-    case kDown: return launch<kKDown>(tm, P, items, s);
-    case kDownGrad: return launch<kKDownGrad>(tm, P, items, s);
-    default: return launch<kKUpGrad>(tm, P, items, s);
+    case kUp: return launch_either<kKUp>(tm, P, P.K, least, most, s);
+    case kDown: return launch_either<kKDown>(tm, P, P.K, least, most, s);
+    case kDownGrad: return launch_either<kKDownGrad>(tm, P, P.K, least, most, s);
+    default: return launch_either<kKUpGrad>(tm, P, P.K, least, most, s);
   }
 }
 
@@ -732,15 +815,15 @@ moe_status_t launch_weight_grad_tc(int rows, int E, int M, int N, moe_dtype_t ou
   P.n_tiles = ceil_div(N, 256);
   P.accumulate = accumulate;
   const bool f32 = out_dt == MOE_F32;
+  P.out_bytes = N * (f32 ? 4 : 2);
   uint32_t box[2] = {64, BK};
   uint64_t da[2] = {m, r}, sa[1] = {m}, db[2] = {n, r}, sb[1] = {n};
-  uint64_t dw[3] = {n, m, (uint64_t)E}, sw[2] = {n, m * n};
-  if (!make_map(&tm.a, dy, 2, da, sa, box, false) || !make_map(&tm.b0, a, 2, db, sb, box, false) ||
-      !make_out_map(&tm.o0, dW, f32, 3, dw, sw, 32))
+  if (!make_map(&tm.a, dy, 2, da, sa, box, false) || !make_map(&tm.b0, a, 2, db, sb, box, false))
     return MOE_ERR_CUDA;
-  const int64_t items = (int64_t)E * P.m_tiles * P.n_tiles;
-  if (items > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
-  return f32 ? launch<kKWeight32>(tm, P, items, s) : launch<kKWeight16>(tm, P, items, s);
+  P.wide = ((uintptr_t)dW & 31u) == 0 && P.out_bytes % 32 == 0;
+  const int64_t items = (int64_t)E * P.m_tiles;
+  return f32 ? launch_either<kKWeight32>(tm, P, rows / E, items, items, s)
+             : launch_either<kKWeight16>(tm, P, rows / E, items, items, s);
 }
 
 }  // namespace moe

@@ -148,6 +148,8 @@ COUNTS = {
     "empty": [0, 0, 0],
     "many": [(7 * e) % 23 for e in range(70)],
     "first-last": [0] * 30 + [40] + [0] * 33 + [3],
+    # enough rows for the tensor-core kernels' wide items, which long dimensions below then take
+    "wide": [257, 0, 300, 1000, 17, 700],
 }
 
 
@@ -174,7 +176,8 @@ def expert_inputs(name, H, I, dtype, seed):
 
 
 EXPERT_SHAPES = [("one", 8, 8), ("edges", 64, 96), ("edges", 264, 520), ("long", 320, 136), ("empty", 64, 64),
-                 ("many", 136, 72), ("first-last", 1032, 256), ("long", 512, 768)]
+                 ("many", 136, 72), ("first-last", 1032, 256), ("long", 512, 768), ("wide", 4104, 6600),
+                 ("wide", 13000, 2056)]
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
@@ -221,9 +224,10 @@ def test_expert_products_and_gradients(M, L, name, H, I, dtype):
 
 @pytest.mark.parametrize("dtype,out", [(torch.bfloat16, torch.float32), (torch.bfloat16, torch.bfloat16),
                                        (torch.float32, torch.float32)])
-@pytest.mark.parametrize("Mm,N", [(72, 200), (256, 256), (520, 264)])
+@pytest.mark.parametrize("Mm,N", [(72, 200), (256, 256), (520, 264), (4104, 2600)])
 def test_weight_grad_accumulates(M, Mm, N, dtype, out):
-    counts = COUNTS["edges"] + [700]
+    # the last size takes the wide items, with a last item of one tile and an expert without rows
+    counts = [2600, 0, 5200] if N > 1000 else COUNTS["edges"] + [700]
     rs, P = runs(counts)
     g = gen(Mm)
     live = torch.zeros(P, 1, dtype=torch.bool, device=DEV)
