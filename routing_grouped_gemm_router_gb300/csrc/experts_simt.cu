@@ -2,8 +2,8 @@
 // tf32 keeps 10 bits of an operand, and a sum of split bf16 products loses the low bits of long
 // reductions).
 //
-// One CTA computes a TM x 128 tile of one expert's product, 16 x 16 threads with TM/16 x 8 sums each:
-// a step of the reduction reads TM/16 + 8 values from shared memory for TM/2 multiply-adds. Operand
+// One CTA computes a TM x 128 tile of one expert's product, 256 threads with 8 x 8 sums each (TM =
+// 128) or 128 with 4 x 8 (TM = 32). Operand
 // tiles of 16 reduction steps are loaded into registers while the previous ones are used (two
 // buffers, one barrier a tile). TM is 128 where experts have many rows; with few, 32-row tiles
 // keep the wasted multiply-adds below the time the weights take from HBM. The FMA pipes bound it.
@@ -12,7 +12,7 @@
 namespace moe {
 namespace esimt {
 
-constexpr int TN = 128, TK = 16, kThreads = 256;
+constexpr int TN = 128, TK = 16;
 constexpr int PAD = 4;
 
 __device__ int g_status;
@@ -23,65 +23,98 @@ __device__ __forceinline__ float sigmoid(float v) { return 1.f / (1.f + expf(-v)
 // index is: into registers, then into shared memory as s[k][row]. Rows from `limit` on and reduction
 // steps from `kmax` on are zeros. Both limits and ld are multiples of 4 along the contiguous index
 // (H and I are multiples of 8; the reduction over an expert's rows runs over the other one).
-template <int ROWS, bool KC>
+template <int ROWS, bool KC, int THREADS>
 struct Tile {
-  static constexpr int N4 = ROWS * TK / 4 / kThreads;  // float4 a thread; 0: half the threads, one
-  static constexpr int COUNT = N4 > 0 ? N4 : 1;
+  static constexpr int COUNT = ROWS * TK / 4 / THREADS;  // float4 a thread
+  static_assert(COUNT >= 1 && COUNT * THREADS * 4 == ROWS * TK, "whole pieces");
   float4 r[COUNT];
   __device__ __forceinline__ void load(const float* __restrict__ p, int64_t ld, int limit, int k0,
                                        int kmax) {
 #pragma unroll
     for (int i = 0; i < COUNT; ++i) {
-      const int f = threadIdx.x + i * kThreads;
+      const int f = threadIdx.x + i * THREADS;
       r[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (N4 == 0 && f >= ROWS * TK / 4) continue;
       const int row = KC ? f / (TK / 4) : f % (ROWS / 4) * 4;
       const int k = KC ? f % (TK / 4) * 4 : f / (ROWS / 4);
       if (row < limit && k0 + k < kmax)
         r[i] = __ldg((const float4*)(KC ? p + row * ld + k0 + k : p + (k0 + k) * ld + row));
     }
   }
-  __device__ __forceinline__ void store(float (*s)[ROWS + PAD]) const {
+  template <int W>
+  __device__ __forceinline__ void store(float (*s)[W], int col0) const {
 #pragma unroll
     for (int i = 0; i < COUNT; ++i) {
-      const int f = threadIdx.x + i * kThreads;
-      if (N4 == 0 && f >= ROWS * TK / 4) continue;
+      const int f = threadIdx.x + i * THREADS;
       if (KC) {
-        const int row = f / (TK / 4), k = f % (TK / 4) * 4;
+        const int row = col0 + f / (TK / 4), k = f % (TK / 4) * 4;
         s[k][row] = r[i].x;
         s[k + 1][row] = r[i].y;
         s[k + 2][row] = r[i].z;
         s[k + 3][row] = r[i].w;
       } else {
-        const int row = f % (ROWS / 4) * 4, k = f / (ROWS / 4);
+        const int row = col0 + f % (ROWS / 4) * 4, k = f / (ROWS / 4);
         *(float4*)&s[k][row] = r[i];
       }
     }
   }
 };
 
-// acc[i][j] += sum over a tile's 16 steps of a[ty * MR + i] * b[column j of this thread]. A thread's
-// eight columns are tx * 4 .. + 3 and 64 + tx * 4 .. + 3.
+// Two fp32 sums that one instruction advances.
+struct F2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void split(F2 a, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a.v));
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+
+// acc[i][j] += sum over a tile's 16 steps of rows ty * MR + 2i, + 1 of a times column j of this
+// thread. Its eight columns are tx * 4 .. + 3 and 64 + tx * 4 .. + 3. Pairs of rows share an
+// instruction, which leaves issue slots for everything else.
 template <int MR, int TM>
 __device__ __forceinline__ void multiply(const float (*a)[TM + PAD], const float (*b)[TN + PAD],
-                                         float (&acc)[MR][8]) {
+                                         F2 (&acc)[MR / 2][8]) {
   const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
 #pragma unroll
   for (int k = 0; k < TK; ++k) {
-    float x[MR], y[8];
+    F2 x[MR / 2];
+    float y[8];
     if constexpr (MR % 4 == 0) {
 #pragma unroll
-      for (int i = 0; i < MR; i += 4) *(float4*)&x[i] = *(const float4*)&a[k][ty * MR + i];
+      for (int i = 0; i < MR; i += 4) {
+        const float4 q = *(const float4*)&a[k][ty * MR + i];
+        x[i / 2] = f2(q.x, q.y);
+        x[i / 2 + 1] = f2(q.z, q.w);
+      }
     } else {
-      *(float2*)x = *(const float2*)&a[k][ty * MR];
+      const float2 q = *(const float2*)&a[k][ty * MR];
+      x[0] = f2(q.x, q.y);
     }
     *(float4*)&y[0] = *(const float4*)&b[k][tx * 4];
     *(float4*)&y[4] = *(const float4*)&b[k][64 + tx * 4];
 #pragma unroll
-    for (int i = 0; i < MR; ++i)
+    for (int j = 0; j < 8; ++j) {
+      const F2 yy = f2(y[j], y[j]);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) acc[i][j] = fmaf(x[i], y[j], acc[i][j]);
+      for (int i = 0; i < MR / 2; ++i) acc[i][j] = fma2(x[i], yy, acc[i][j]);
+    }
   }
+}
+template <int MR>
+__device__ __forceinline__ void unpair(const F2 (&p)[MR / 2][8], float (&acc)[MR][8]) {
+#pragma unroll
+  for (int i = 0; i < MR / 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) split(p[i][j], acc[2 * i][j], acc[2 * i + 1][j]);
 }
 
 struct Rows {
@@ -91,15 +124,19 @@ struct Rows {
 // C[rows, N] = A[rows, K] * W[e], W[e] given as [N, K] (up, down) or [K, N] (their gradients).
 // The columns of an up tile are 64 gate rows of W13 and the same 64 up rows. Row tiles after the last
 // expert's cover the rows past the experts' runs, which are zeroed.
+template <int TM>
+constexpr int kThreadsOf = TM == 128 ? 256 : 128;
+
 template <int KIND, int TM>
-__global__ void __launch_bounds__(kThreads, 2) product_kernel(
+__global__ void __launch_bounds__(kThreadsOf<TM>, TM == 128 ? 2 : 4) product_kernel(
     const float* __restrict__ A, const float* __restrict__ W, const float* __restrict__ h13,
     const int32_t* __restrict__ counts, int E, int rows, int N, int K, float* __restrict__ out,
     float* __restrict__ act) {
   pdl_wait();
   pdl_trigger();
   constexpr bool TRANS = KIND == kDownGrad || KIND == kUpGrad;
-  constexpr int MR = TM / 16;
+  constexpr int kThreads = kThreadsOf<TM>;
+  constexpr int MR = TM / (kThreads / 16);
   constexpr int CN = KIND == kUp ? 64 : 128;  // output columns of a tile
   __shared__ int start[kMaxExperts + 1], cnt[kMaxExperts];
   __shared__ Rows tile;
@@ -140,13 +177,13 @@ __global__ void __launch_bounds__(kThreads, 2) product_kernel(
   const Rows tl = tile;
   if (tl.pad <= 0) return;
   const int n0 = blockIdx.y * CN;
-  float acc[MR][8] = {};
+  F2 sums[MR / 2][8] = {};
   if (tl.e >= 0) {
     const float* We = W + (int64_t)tl.e * (KIND == kUp ? 2 : 1) * N * K;
     const float* Ar = A + (int64_t)tl.row * K;
-    Tile<TM, true> ta;
+    Tile<TM, true, kThreads> ta;
     // two half tiles of columns: gate and up rows, or 128 columns in a row
-    Tile<64, !TRANS> tb[2];
+    Tile<64, !TRANS, kThreads> tb[2];
     const float* b0 = TRANS ? We + n0 : We + (int64_t)n0 * K;
     const float* b1 = TRANS ? b0 + 64 : KIND == kUp ? b0 + (int64_t)N * K : b0 + (int64_t)64 * K;
     const int64_t ldb = TRANS ? N : K;
@@ -157,22 +194,9 @@ __global__ void __launch_bounds__(kThreads, 2) product_kernel(
       tb[1].load(b1, ldb, lim1, k0, K);
     };
     auto store = [&](int s) {
-      ta.store(sA[s]);
-      // each half of the columns: rows of 64 values inside the 128-wide tile
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int f = threadIdx.x;
-        if (!TRANS) {
-          const int row = f / (TK / 4), k = f % (TK / 4) * 4;
-          sB[s][k][h * 64 + row] = tb[h].r[0].x;
-          sB[s][k + 1][h * 64 + row] = tb[h].r[0].y;
-          sB[s][k + 2][h * 64 + row] = tb[h].r[0].z;
-          sB[s][k + 3][h * 64 + row] = tb[h].r[0].w;
-        } else {
-          const int row = f % 16 * 4, k = f / 16;
-          *(float4*)&sB[s][k][h * 64 + row] = tb[h].r[0];
-        }
-      }
+      ta.store(sA[s], 0);
+      tb[0].store(sB[s], 0);
+      tb[1].store(sB[s], 64);
     };
     load(0);
     store(0);
@@ -181,12 +205,14 @@ __global__ void __launch_bounds__(kThreads, 2) product_kernel(
     for (int k0 = 0; k0 < K; k0 += TK) {
       const bool more = k0 + TK < K;
       if (more) load(k0 + TK);
-      multiply<MR, TM>(sA[s], sB[s], acc);
+      multiply<MR, TM>(sA[s], sB[s], sums);
       if (more) store(s ^ 1);
       __syncthreads();
       s ^= 1;
     }
   }
+  float acc[MR][8];
+  unpair<MR>(sums, acc);
   const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
 #pragma unroll
   for (int i = 0; i < MR; ++i) {
@@ -237,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 2) product_kernel(
 }
 
 // dW[e][m, n] (+)= sum over expert e's rows p of dy[p, m] a[p, n].
-__global__ void __launch_bounds__(kThreads, 2) weight_grad_kernel(
+__global__ void __launch_bounds__(256, 2) weight_grad_kernel(
     const float* __restrict__ dy, const float* __restrict__ a, const int32_t* __restrict__ counts,
     int E, int rows, int M, int N, int accumulate, float* __restrict__ dW) {
   pdl_wait();
@@ -253,15 +279,15 @@ __global__ void __launch_bounds__(kThreads, 2) weight_grad_kernel(
   const int m0 = rest / tn * TN, n0 = rest % tn * TN;
   const int np = cnt[e];
   if (np == 0 && accumulate) return;
-  float acc[8][8] = {};
+  F2 sums[4][8] = {};
   if (np > 0) {
     const float* dp = dy + (int64_t)start[e] * M + m0;
     const float* ap = a + (int64_t)start[e] * N + n0;
-    Tile<TN, false> ta, tb;
+    Tile<TN, false, 256> ta, tb;
     ta.load(dp, M, M - m0, 0, np);
     tb.load(ap, N, N - n0, 0, np);
-    ta.store(sA[0]);
-    tb.store(sB[0]);
+    ta.store(sA[0], 0);
+    tb.store(sB[0], 0);
     __syncthreads();
     int s = 0;
     for (int k0 = 0; k0 < np; k0 += TK) {
@@ -270,15 +296,17 @@ __global__ void __launch_bounds__(kThreads, 2) weight_grad_kernel(
         ta.load(dp, M, M - m0, k0 + TK, np);
         tb.load(ap, N, N - n0, k0 + TK, np);
       }
-      multiply<8, TN>(sA[s], sB[s], acc);
+      multiply<8, TN>(sA[s], sB[s], sums);
       if (more) {
-        ta.store(sA[s ^ 1]);
-        tb.store(sB[s ^ 1]);
+        ta.store(sA[s ^ 1], 0);
+        tb.store(sB[s ^ 1], 0);
       }
       __syncthreads();
       s ^= 1;
     }
   }
+  float acc[8][8];
+  unpair<8>(sums, acc);
   const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -304,10 +332,10 @@ __global__ void __launch_bounds__(kThreads, 2) weight_grad_kernel(
 using namespace esimt;
 
 // 32-row tiles below this many buffer rows an expert, 128-row tiles from it on. Measured with 64
-// experts of H = 2048, I = 1408, forward and backward: 31 rows an expert 3.95 against 6.91 ms, 63 rows
-// 7.28 and 7.57, 79 rows 8.81 and 7.89, 143 rows 15.5 and 11.6. (1024 rows an expert: 46.6 TFLOP/s,
-// 0.84 of a batched library product of the same buckets.)
-constexpr int kManyRows = 64;
+// experts of H = 2048, I = 1408, forward and backward: 31 rows an expert 2.70 against 5.98 ms, 79 rows
+// 5.91 and 6.92, 143 rows 10.35 and 10.27; 8 experts of 1038 rows 9.42 and 8.22 (51.7 TFLOP/s, 0.93 of
+// a batched library product over the same rows).
+constexpr int kManyRows = 128;
 
 moe_status_t launch_expert_product_simt(ExpertProduct kind, const moe_experts_t& c, const void* a,
                                         const void* w, const float* h13, const int32_t* counts,
@@ -321,7 +349,7 @@ moe_status_t launch_expert_product_simt(ExpertProduct kind, const moe_experts_t&
   const dim3 grid(2 * ceil_div(c.rows, tm) + c.E, ceil_div(N, kind == kUp ? 64 : 128));
   if (grid.y > 65535) return MOE_ERR_UNSUPPORTED;
   auto go = [&](auto kern) {
-    return launch_k(kern, grid, dim3(kThreads), 0, s, (const float*)a, (const float*)w, h13, counts,
+    return launch_k(kern, grid, dim3(many ? 256 : 128), 0, s, (const float*)a, (const float*)w, h13, counts,
                     c.E, c.rows, N, K, (float*)out, (float*)act);
   };
   switch (kind) {
@@ -338,7 +366,7 @@ moe_status_t launch_weight_grad_simt(int rows, int E, int M, int N, int accumula
                                      void* dW, cudaStream_t s) {
   const int64_t tiles = (int64_t)E * ceil_div(M, TN) * ceil_div(N, TN);
   if (tiles > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
-  return launch_k(weight_grad_kernel, dim3((unsigned)tiles), dim3(kThreads), 0, s,
+  return launch_k(weight_grad_kernel, dim3((unsigned)tiles), dim3(256), 0, s,
                   (const float*)dy, (const float*)a, counts, E, rows, M, N, accumulate, (float*)dW);
 }
 

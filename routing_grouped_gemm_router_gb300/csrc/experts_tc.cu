@@ -97,6 +97,7 @@ struct Params {
 
 struct Maps {
   CUtensorMap a, b0, b1;
+  CUtensorMap a16, b16;  // weight: 16-row boxes, for the end of a reduction
 };
 
 // M/N-major operand tile: 128-byte swizzled rows of 64 elements along M or N, one row a K index;
@@ -314,26 +315,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<KIND, NH>::kT
       bool ok = true;
       for (int w = pair; w < total && ok; w += num_pairs) {
         const Item it = item_of<KIND, NH>(w, P, start, cnt, pre);
-        const uint32_t bytes = 2u * (A_BYTES + it.nh * B_BYTES) - (it.live1 ? 0u : (uint32_t)A_BYTES);
+        const uint32_t row_bytes = 2u * (A_BYTES + it.nh * B_BYTES) - (it.live1 ? 0u : (uint32_t)A_BYTES);
         for (int kb = 0; kb < it.num_kb; ++kb) {
           if (!wait_bounded(&empty[s], phase ^ 1u, abort_flag, status)) {
             ok = false;
             break;
           }
           const uint32_t fl = cluster_addr(&full[s], 0);
-          if (leader) mbar_expect_tx(&full[s], bytes);
           uint8_t* a = sA + s * A_BYTES;
           uint8_t* b = sB + s * LY::kStageB;
           if (R::weight) {
+            // the last stage of the reduction: as many 16-row steps as it has (dW of 32 experts of
+            // 5760 x 2880 over 1 to 8 rows each: 298 -> 289 us)
+            const int left = it.cnt - kb * BK, steps = left > 48 ? 4 : (left + 15) / 16;
+            if (leader) mbar_expect_tx(&full[s], 2u * (1 + it.nh) * (steps * 4096u));
             const int y = it.row0 + kb * BK, m = it.m0 + (int)rank * 128;
-            tma_2d_pair(a, &TM.a, fl, m, y);
-            tma_2d_pair(a + CHUNK, &TM.a, fl, m + 64, y);
-            for (int h = 0; h < it.nh; ++h, b += B_BYTES) {
-              const int n = (it.n + h) * 256 + (int)rank * 128;
-              tma_2d_pair(b, &TM.b0, fl, n, y);
-              tma_2d_pair(b + CHUNK, &TM.b0, fl, n + 64, y);
-            }
+            auto two = [&](uint8_t* to, const CUtensorMap* whole, const CUtensorMap* part, int x) {
+              if (steps == 4) {
+                tma_2d_pair(to, whole, fl, x, y);
+                tma_2d_pair(to + CHUNK, whole, fl, x + 64, y);
+              } else {
+                for (int j = 0; j < steps; ++j) {
+                  tma_2d_pair(to + j * 2048, part, fl, x, y + 16 * j);
+                  tma_2d_pair(to + CHUNK + j * 2048, part, fl, x + 64, y + 16 * j);
+                }
+              }
+            };
+            two(a, &TM.a, &TM.a16, m);
+            for (int h = 0; h < it.nh; ++h, b += B_BYTES)
+              two(b, &TM.b0, &TM.b16, (it.n + h) * 256 + (int)rank * 128);
           } else {
+            if (leader) mbar_expect_tx(&full[s], row_bytes);
             // the peer's rows of a half-filled tile are neither loaded nor stored
             if (leader || it.live1) tma_2d_pair(a, &TM.a, fl, kb * BK, it.m0 + (int)rank * 128);
             for (int h = 0; h < it.nh; ++h, b += B_BYTES) {
@@ -818,8 +830,10 @@ moe_status_t launch_weight_grad_tc(int rows, int E, int M, int N, moe_dtype_t ou
   P.out_bytes = N * (f32 ? 4 : 2);
   uint32_t box[2] = {64, BK};
   uint64_t da[2] = {m, r}, sa[1] = {m}, db[2] = {n, r}, sb[1] = {n};
-  if (!make_map(&tm.a, dy, 2, da, sa, box, false) || !make_map(&tm.b0, a, 2, db, sb, box, false))
-    return MOE_ERR_CUDA;
+  bool ok = make_map(&tm.a, dy, 2, da, sa, box, false) && make_map(&tm.b0, a, 2, db, sb, box, false);
+  box[1] = 16;
+  ok = ok && make_map(&tm.a16, dy, 2, da, sa, box, false) && make_map(&tm.b16, a, 2, db, sb, box, false);
+  if (!ok) return MOE_ERR_CUDA;
   P.wide = ((uintptr_t)dW & 31u) == 0 && P.out_bytes % 32 == 0;
   const int64_t items = (int64_t)E * P.m_tiles;
   return f32 ? launch_either<kKWeight32>(tm, P, rows / E, items, items, s)
