@@ -168,3 +168,16 @@ def test_buffer_rows(M):
     assert M.buffer_rows(1, 1, 1) == 16
     assert M.buffer_rows(4096, 8, 256) == (4096 * 8 + 256 * 15) // 16 * 16
     assert M.buffer_rows(3, 2, 512) == 6 * 16
+
+
+def test_block_refuses_parameters_that_do_not_fit(M):
+    from routing_grouped_gemm_router_gb300.sparse_block import SparseBlock, SparseStack
+    g = torch.ones(64)
+    ok = dict(Wg=torch.zeros(4, 64), W13=torch.zeros(4, 96, 64), W2=torch.zeros(4, 64, 48))
+    SparseBlock(**ok, gamma_in=g, gamma_out=g, k=2)
+    for kw in (dict(W13=torch.zeros(5, 96, 64)), dict(W2=torch.zeros(4, 64, 40)), dict(W2=torch.zeros(4, 72, 48)),
+               dict(W13=torch.zeros(4, 96, 72))):
+        with pytest.raises(ValueError):
+            SparseBlock(**{**ok, **kw}, gamma_in=g, gamma_out=g, k=2)
+    with pytest.raises(ValueError):
+        SparseStack([])
