@@ -55,7 +55,7 @@ class SparseBlock:
         logits = torch.empty(T, self.E, dtype=torch.float32, device=h.device)
         ids = torch.empty(T, kk, dtype=torch.int32, device=h.device)
         w = torch.empty(T, kk, dtype=torch.float32, device=h.device)
-        cfg = L.make_config(T, self.H, self.I, self.E, self.k, ops._DTYPES[h.dtype], self.mode,
+        cfg = L.make_config(T, self.H, self.I, self.E, self.k, L.MOE_BF16 if h.dtype == torch.bfloat16 else L.MOE_F32, self.mode,
                             self.renormalize, self.router_scale, self.n_group, self.topk_group,
                             self.logit_bias, self.select_bias, n_shared=self.n_shared)
         L.moe_route(cfg, h, self.Wg, logits, ids, w)
