@@ -345,13 +345,15 @@ struct Outs {
 
 // ------------------------------------------------------------------- backward
 // JOIN: gradients of the join (and of the next norm, if gamma_next); otherwise of the norm of x,
-// with dres added. Row tensors, those that are there: dh, what the norm read (x or out), dres,
+// with dres added. BOTH: a next norm and dres are both there, as everywhere inside a stack (known at
+// compile time that takes 7 to 24 % off: 8192 x 4096 with a token gate 88 -> 82 us, 8192 x 7168 with a
+// channel gate 215 -> 164). Row tensors, those that are there: dh, what the norm read (x or out), dres,
 // y, full gate. A token gate (and the scale) is a factor of a whole row and a channel gate's scale
 // one of a whole column, so they are taken out of the sums:
 //   q = sum d yn gp (gate):  dgate_token = scale q,  mean(b yn) = scale (gate) q / H;
 // and with d = d0 - m x, m from the next norm's own reduction, q = sum d0 yn gp - m sum x yn gp: the
 // three sums of a row are taken together, and one barrier a row is enough.
-template <typename T, int VPT, bool JOIN, int GATE>
+template <typename T, int VPT, bool JOIN, int GATE, bool BOTH>
 __global__ void __launch_bounds__(kThreadsOf<VPT>)
     backward_kernel(const __grid_constant__ Shape S,
                                                                const BlockNormArgs A, int kinds,
@@ -366,10 +368,10 @@ __global__ void __launch_bounds__(kThreadsOf<VPT>)
   pdl_trigger();
   ring.start();
   int turn = 0;
-  const bool next = !JOIN || A.gamma_next;
+  const bool next = BOTH || !JOIN || A.gamma_next, res = BOTH || A.dres;
   const float* gamma_n = JOIN ? A.gamma_next : A.gamma;
   const float* rstd_n = JOIN ? A.rstd_out_in : A.rstd_y_in;
-  const int i_res = next ? 2 : 0, i_y = i_res + (A.dres ? 1 : 0);
+  const int i_res = next ? 2 : 0, i_y = i_res + (res ? 1 : 0);
   const F2 offset = dup(S.offset), zero = dup(0.f);
   F2 sn[VPT][4], sp[JOIN ? VPT : 1][4], sg[CHANNEL ? VPT : 1][4];
 #pragma unroll
@@ -423,7 +425,7 @@ __global__ void __launch_bounds__(kThreadsOf<VPT>)
           d[v][i] = d[v][i] * rn2;
         }
       }
-      if (A.dres) {
+      if (res) {
         Chunk<T> rq;
         F2 f[4];
         ring.get(rq, i_res, v, tl);
@@ -681,7 +683,13 @@ static moe_status_t backward(const moe_block_t& c, const BlockNormArgs& a, cudaS
     return run(kern, S, dtype_size(c.dtype), least, v * dtype_size(c.dtype) <= 8, kMaxCtas, blocks, s, a,
                kinds, outs);
   };
-  const moe_status_t st = BNORM_PICK(backward_kernel, JOIN, GATE);
+  moe_status_t st;
+  if constexpr (JOIN) {
+    st = next && a.dres ? BNORM_PICK(backward_kernel, true, GATE, true)
+                        : BNORM_PICK(backward_kernel, true, GATE, false);
+  } else {
+    st = BNORM_PICK(backward_kernel, false, MOE_GATE_NONE, false);
+  }
   if (st != MOE_OK || blocks == 1) return st;
   return launch_k(column_sum_kernel, dim3(ceil_div(kinds * c.H, 32)), dim3(1024), 0, s,
                   (const float*)a.ws, blocks, kinds, c.H, outs);
