@@ -14,9 +14,9 @@ namespace moe {
 namespace dispatch {
 
 // ------------------------------------------------------------------- permute
-// One warp a buffer row: the sorted table gives the slot, the slot its token. Reads of a token
-// row by its k copies hit L2. Rows of no slot are written as zeros, so that the expert products
-// may run over whole 16-row steps.
+// One warp a buffer row: the sorted table gives the slot, the slot its token. Rows of no slot are
+// written as zeros, so that the expert products may run over whole 16-row steps. Written rows are
+// marked to leave L2 first, for the token rows that are read k times to stay.
 __global__ void __launch_bounds__(256) permute_kernel(const uint4* __restrict__ x,
                                                       const int32_t* __restrict__ ids,
                                                       const int32_t* __restrict__ sid, int n,
@@ -45,12 +45,68 @@ __global__ void __launch_bounds__(256) permute_kernel(const uint4* __restrict__ 
     int v = lane;
     for (; v + 96 < vec; v += 128) {
       const uint4 a = src[v], b = src[v + 32], c = src[v + 64], d = src[v + 96];
-      dst[v] = a;
-      dst[v + 32] = b;
-      dst[v + 64] = c;
-      dst[v + 96] = d;
+      __stcs(dst + (v), a);
+      __stcs(dst + (v + 32), b);
+      __stcs(dst + (v + 64), c);
+      __stcs(dst + (v + 96), d);
     }
-    for (; v < vec; v += 32) dst[v] = src[v];
+    for (; v < vec; v += 32) __stcs(dst + v, src[v]);
+  }
+}
+
+// Where the copies outgrow L2, token rows would come from HBM several times that way (199 MB read for
+// 58 MB of tokens: 114 us for 4096 x 7168 with 8 slots each). So positions are written first, by a
+// kernel of their own, and then a thread reads a 16-byte piece of a token once and writes it to the
+// token's k rows: 89 us, 5.9 TB/s written. The first blocks write the rows of no slot.
+constexpr size_t kTokenMajorFrom = (size_t)1 << 27;  // bytes of xs; below, one kernel is quicker
+constexpr int kZeroRows = 64;                        // table entries a zeroing block looks at
+
+__global__ void __launch_bounds__(256) positions_kernel(const int32_t* __restrict__ ids,
+                                                        const int32_t* __restrict__ sid, int n,
+                                                        int E, int rows, int32_t* __restrict__ pos) {
+  pdl_wait();
+  pdl_trigger();
+  const int first = blockIdx.x * blockDim.x + threadIdx.x, step = gridDim.x * blockDim.x;
+  for (int r = first; r < n; r += step) {
+    const int e = ids[r];
+    if (e < 0 || e >= E) pos[r] = -1;
+  }
+  for (int p = first; p < rows; p += step) {
+    const int r = sid[p];
+    if (r >= 0 && r < n) pos[r] = p;
+  }
+}
+
+// Zeros into the rows of no slot among table entries block * kZeroRows ..., a warp a row.
+__device__ __forceinline__ void zero_rows(int block, const int32_t* __restrict__ sid, int n, int rows,
+                                          int vec, uint4* __restrict__ xs) {
+  const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  const int p0 = block * kZeroRows;
+  for (int p = p0 + (threadIdx.x >> 5); p < min(p0 + kZeroRows, rows); p += warps) {
+    const int r = sid[p];
+    if (r >= 0 && r < n) continue;
+    for (int v = lane; v < vec; v += 32) __stcs(xs + (int64_t)p * vec + v, make_uint4(0, 0, 0, 0));
+  }
+}
+
+__global__ void __launch_bounds__(256) permute_tokens_kernel(
+    const uint4* __restrict__ x, const int32_t* __restrict__ sid, const int32_t* __restrict__ pos,
+    int Tn, int k, int rows, int vec, int parts, uint4* __restrict__ xs) {
+  pdl_wait();
+  pdl_trigger();
+  const int zeroing = (rows + kZeroRows - 1) / kZeroRows;
+  if ((int)blockIdx.x < zeroing) {
+    zero_rows(blockIdx.x, sid, Tn * k, rows, vec, xs);
+    return;
+  }
+  const int b = blockIdx.x - zeroing;
+  const int64_t t = b / parts;
+  const int v = b % parts * blockDim.x + threadIdx.x;
+  if (v >= vec) return;
+  const uint4 q = __ldcs(x + t * vec + v);
+  for (int j = 0; j < k; ++j) {
+    const int p = __ldg(pos + t * k + j);
+    if (p >= 0 && p < rows) __stcs(xs + (int64_t)p * vec + v, q);
   }
 }
 
@@ -94,13 +150,12 @@ __global__ void __launch_bounds__(256) slot_sum_kernel(const uint4* __restrict__
 }
 
 // ------------------------------------------------- gradients of the weighted sum
-// Blocks 0..T-1: one a token. Its slots are taken four at a time: a thread loads its 16-byte piece
+// One block a token. Its slots are taken four at a time: a thread loads its 16-byte piece
 // of dout and of the four ys rows before it uses any, so that four rows are in flight; the dot
 // products of all slots meet in shared memory once, at the end. (dout comes from L2 again for
-// the next four.) The blocks after them write zeros into rows of no slot.
+// the next four.) The first blocks write zeros into rows of no slot.
 constexpr int kUbThreads = 256;
 constexpr int kBatch = 4;
-constexpr int kZeroRows = 64;  // table entries a zeroing block looks at
 
 template <typename T>
 __global__ void __launch_bounds__(kUbThreads) unpermute_backward_kernel(
@@ -111,18 +166,13 @@ __global__ void __launch_bounds__(kUbThreads) unpermute_backward_kernel(
   pdl_trigger();
   constexpr int W = 16 / sizeof(T);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  if ((int)blockIdx.x >= Tn) {
-    const int p0 = ((int)blockIdx.x - Tn) * kZeroRows;
-    const uint4 z = make_uint4(0, 0, 0, 0);
-    for (int p = p0 + warp; p < min(p0 + kZeroRows, rows); p += warps) {
-      const int r = sid[p];
-      if (r >= 0 && r < Tn * k) continue;
-      for (int v = lane; v < vec; v += 32) dys[(int64_t)p * vec + v] = z;
-    }
+  const int zeroing = (rows + kZeroRows - 1) / kZeroRows;
+  if ((int)blockIdx.x < zeroing) {
+    zero_rows(blockIdx.x, sid, Tn * k, rows, vec, dys);
     return;
   }
   __shared__ float dots[32][kUbThreads / 32];
-  const int64_t t = blockIdx.x;
+  const int64_t t = (int)blockIdx.x - zeroing;
   const uint4* drow = dout + t * vec;
   for (int j0 = 0; j0 < k; j0 += kBatch) {
     const uint4* yrow[kBatch];
@@ -157,7 +207,7 @@ __global__ void __launch_bounds__(kUbThreads) unpermute_backward_kernel(
           dot[j] = fmaf(d[i], y[i], dot[j]);
           y[i] = d[i] * wj[j];
         }
-        orow[j][v] = Vec<T>::pack(y);
+        __stcs(orow[j] + v, Vec<T>::pack(y));
       }
     }
 #pragma unroll
@@ -182,6 +232,17 @@ moe_status_t launch_permute(const void* x, const int32_t* ids, const int32_t* si
                             int E, int H, moe_dtype_t dt, int rows, void* xs, int32_t* pos,
                             cudaStream_t s) {
   const int vec = H * (int)dtype_size(dt) / 16;
+  const int threads = vec >= 256 ? 256 : std::max(32, ceil_div(vec, 32) * 32);
+  const int parts = ceil_div(vec, threads);
+  const int64_t grid = (int64_t)T * parts + ceil_div(rows, kZeroRows);
+  if ((size_t)rows * vec * 16 >= kTokenMajorFrom && grid <= 0x7fffffff) {
+    const int blocks = std::min(ceil_div(std::max(rows, T * k), 256), num_sms() * 4);
+    const moe_status_t st = launch_k(positions_kernel, dim3(blocks), dim3(256), 0, s, ids, sid, T * k, E,
+                                     rows, pos);
+    if (st != MOE_OK) return st;
+    return launch_k(permute_tokens_kernel, dim3((unsigned)grid), dim3(threads), 0, s, (const uint4*)x, sid,
+                    (const int32_t*)pos, T, k, rows, vec, parts, (uint4*)xs);
+  }
   const int blocks = std::min(ceil_div(rows, 8), num_sms() * 8);
   return launch_k(permute_kernel, dim3(blocks), dim3(256), 0, s, (const uint4*)x, ids, sid, T * k,
                   k, E, rows, vec, (uint4*)xs, pos);

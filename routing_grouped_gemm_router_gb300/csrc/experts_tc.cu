@@ -19,7 +19,8 @@
 // below), of 128 bytes a clock in all. So the epilogue keeps out of it: a thread holds one row of a
 // tile and stores (and, in down_grad, loads) whole 32-byte sectors of it directly. Measured with
 // 1024 rows an expert, tiles staged through shared memory for full lines took 5 % longer with wide
-// items on and off, whether the TMA or the threads stored them.
+// items on and off, whether the TMA or the threads stored them. (The weight gradients' narrow form,
+// whose reductions are short and results large, is the exception: see there.)
 //
 // Roles in each CTA of a pair: warp 0 issues the TMA loads into a ring of stages, warp 1 of the
 // leader issues the MMAs, the others are the epilogue. Tensor memory holds two 256-column
@@ -52,6 +53,8 @@ constexpr int A_BYTES = 128 * 128;
 constexpr int B_BYTES = 128 * 128;   // of one 256-column tile
 constexpr int CHUNK = 64 * 128;      // one 64-column box of an M/N-major operand: 64 K rows x 128 B
 
+constexpr int OUT_BYTES = 32 * 128;  // a staged tile of dW: 32 rows of 128 bytes
+
 template <int KIND>
 struct Traits {
   static constexpr bool weight = KIND >= kKWeight32;
@@ -63,13 +66,15 @@ struct Traits {
 
 template <int KIND, int NH>
 struct Layout {
-  static constexpr int kStages = NH == 2 ? 4 : 6;
+  static constexpr bool staged = Traits<KIND>::weight && NH == 1;  // dW leaves through the TMA
+  static constexpr int kStages = NH == 2 ? 4 : staged ? 5 : 6;
   static constexpr int kEpiWarps = 8;  // two a 32-lane quarter of tensor memory
   static constexpr int kThreads = 64 + 32 * kEpiWarps;
   static constexpr int kStageB = NH * B_BYTES;
   static constexpr size_t a = 0;
   static constexpr size_t b = a + (size_t)kStages * A_BYTES;
-  static constexpr size_t bars = b + (size_t)kStages * kStageB;
+  static constexpr size_t out = b + (size_t)kStages * kStageB;
+  static constexpr size_t bars = out + (staged ? (size_t)kEpiWarps * OUT_BYTES : 0);
   static constexpr size_t misc = bars + (2 * kStages + 5) * 8;
   static constexpr size_t start = misc + 16;
   static constexpr size_t cnt = start + (kMaxExperts + 1) * 4;
@@ -77,7 +82,8 @@ struct Layout {
   static constexpr size_t end = pre + (kMaxExperts + 1) * 4;
   static constexpr size_t bytes = 1024 + end;
 };
-static_assert(Layout<kKUp, 1>::bytes <= 232448 && Layout<kKUp, 2>::bytes <= 232448, "shared memory");
+static_assert(Layout<kKUp, 1>::bytes <= 232448 && Layout<kKUp, 2>::bytes <= 232448 &&
+                  Layout<kKWeight32, 1>::bytes <= 232448, "shared memory");
 
 struct Params {
   const int32_t* counts;
@@ -98,6 +104,7 @@ struct Params {
 struct Maps {
   CUtensorMap a, b0, b1;
   CUtensorMap a16, b16;  // weight: 16-row boxes, for the end of a reduction
+  CUtensorMap o;         // weight: dW in 32-row boxes of 128 bytes
 };
 
 // M/N-major operand tile: 128-byte swizzled rows of 64 elements along M or N, one row a K index;
@@ -112,6 +119,26 @@ __device__ __forceinline__ uint64_t mn_desc(uint32_t saddr) {
   return d;
 }
 
+__device__ __forceinline__ void store_3d(const CUtensorMap* tm, const void* src, int c0, int c1,
+                                         int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+          (uint64_t)tm),
+      "r"(c0), "r"(c1), "r"(c2), "r"(su32(src))
+      : "memory");
+}
+__device__ __forceinline__ void add_3d(const CUtensorMap* tm, const void* src, int c0, int c1,
+                                       int c2) {
+  asm volatile(
+      "cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], "
+      "[%4];" ::"l"((uint64_t)tm),
+      "r"(c0), "r"(c1), "r"(c2), "r"(su32(src))
+      : "memory");
+}
+// The 16-byte piece c of row r of a staged tile (128-byte swizzle, as its map has it).
+__device__ __forceinline__ uint4* piece(uint8_t* tile, int r, int c) {
+  return reinterpret_cast<uint4*>(tile + r * 128 + ((c ^ (r & 7)) << 4));
+}
 // Whether a phase has completed, without waiting.
 __device__ __forceinline__ bool mbar_test(uint64_t* b, uint32_t parity) {
   uint32_t ok;
@@ -166,6 +193,21 @@ __device__ __forceinline__ void put64(void* p, const uint32_t* v, bool wide, int
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = v[8 * h + i];
     put32((uint8_t*)p + 32 * h, x, wide, n - 2 * h);
+  }
+}
+
+// Thirty-two fp32 values plus the bf16 ones at p, in fp32: the sum is rounded once.
+__device__ __forceinline__ void add_old(uint32_t (&v)[32], const uint8_t* p, bool wide, int n) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint32_t o[8];
+    get32(p + 32 * i, o, wide, n - 2 * i);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int x = 16 * i + 2 * j;
+      v[x] = __float_as_uint(__uint_as_float(v[x]) + __uint_as_float(o[j] << 16));
+      v[x + 1] = __float_as_uint(__uint_as_float(v[x + 1]) + __uint_as_float(o[j] & 0xFFFF0000u));
+    }
   }
 }
 
@@ -592,6 +634,55 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<KIND, NH>::kT
               put64(act + (int64_t)col * 2, ap, wide, k);
             }
           }
+        } else if (LY::staged && some) {
+          // dW, often short reductions under large results, where the writes bound: whole 128-byte
+          // lines leave through the TMA, which also clips ragged edges and adds to fp32. fp32 dW of 64
+          // experts of 4096 x 2048: over 8 rows each 339 us (6.3 TB/s), 444 from registers; over 512 rows
+          // 566 and 582; from 1024 on the two meet.
+          constexpr int W = KIND == kKWeight32 ? 32 : 64;
+          uint8_t* const t = smem + LY::out + (size_t)(warp - 2) * OUT_BYTES;
+          const int n0 = n * 256;
+#pragma unroll 1
+          for (int c = part * kCols; c < (part + 1) * kCols; c += W) {
+            const int col = n0 + c;
+            if (col >= P.N) break;
+            // the tile's last store has been read
+            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            __syncwarp();
+#pragma unroll
+            for (int x = 0; x < W; x += 32) {
+              uint32_t v[32];
+              if (computed) {
+                tmem_ld32(tb + c + x, v);
+                tmem_ld_wait();
+              } else {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = 0;
+              }
+              if (KIND == kKWeight32) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  *piece(t, lane, i) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+              } else {
+                if (P.accumulate && store) add_old(v, out + (int64_t)(col + x) * 2, wide, left(col + x, 2));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  uint32_t p4[4];
+#pragma unroll
+                  for (int j = 0; j < 4; ++j)
+                    p4[j] = pack_bf16(__uint_as_float(v[8 * i + 2 * j]), __uint_as_float(v[8 * i + 2 * j + 1]));
+                  *piece(t, lane, x / 8 + i) = make_uint4(p4[0], p4[1], p4[2], p4[3]);
+                }
+              }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              if (KIND == kKWeight32 && P.accumulate) add_3d(&TM.o, t, col, m, it.e);
+              else store_3d(&TM.o, t, col, m, it.e);
+              asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            }
+          }
         } else if (some) {  // down, up_grad, dW
           const int n0 = n * 256;
 #pragma unroll 1
@@ -625,19 +716,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<KIND, NH>::kT
               put64(out + (int64_t)col * 4 + 64, v + 16, wide, k - 4);
             } else {
               const int k = left(col, 2);
-              if (R::weight && P.accumulate) {  // one rounding of the sum
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                  uint32_t o[8];
-                  get32(out + (int64_t)col * 2 + 32 * i, o, wide, k - 2 * i);
-#pragma unroll
-                  for (int j = 0; j < 8; ++j) {
-                    const int x = 16 * i + 2 * j;
-                    v[x] = __float_as_uint(__uint_as_float(v[x]) + __uint_as_float(o[j] << 16));
-                    v[x + 1] = __float_as_uint(__uint_as_float(v[x + 1]) + __uint_as_float(o[j] & 0xFFFF0000u));
-                  }
-                }
-              }
+              if (R::weight && P.accumulate) add_old(v, out + (int64_t)col * 2, wide, k);
               uint32_t pr[16];
 #pragma unroll
               for (int i = 0; i < 16; ++i)
@@ -657,6 +736,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<KIND, NH>::kT
           if (NH == 1) acc ^= 1;
         }
       }
+    }
+    if (LY::staged) {
+      if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+      __syncwarp();
     }
   }
 
@@ -833,6 +916,14 @@ moe_status_t launch_weight_grad_tc(int rows, int E, int M, int N, moe_dtype_t ou
   bool ok = make_map(&tm.a, dy, 2, da, sa, box, false) && make_map(&tm.b0, a, 2, db, sb, box, false);
   box[1] = 16;
   ok = ok && make_map(&tm.a16, dy, 2, da, sa, box, false) && make_map(&tm.b16, a, 2, db, sb, box, false);
+  {
+    auto fn = encode_fn();
+    cuuint64_t d[3] = {n, m, (uint64_t)E}, st[2] = {n * (f32 ? 4 : 2), m * n * (f32 ? 4 : 2)};
+    cuuint32_t obox[3] = {f32 ? 32u : 64u, 32u, 1u}, one[3] = {1, 1, 1};
+    ok = ok && fn && fn(&tm.o, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                        dW, d, st, obox, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  }
   if (!ok) return MOE_ERR_CUDA;
   P.wide = ((uintptr_t)dW & 31u) == 0 && P.out_bytes % 32 == 0;
   const int64_t items = (int64_t)E * P.m_tiles;

@@ -82,7 +82,7 @@ def table(ids, E, P):
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("T,k,E,H,drop", [
     (1, 1, 1, 8, None), (1, 4, 128, 2880, None), (7, 3, 5, 264, "some"), (3, 2, 4, 64, "all"),
-    (33, 32, 40, 72, "some"), (130, 2, 300, 1000, None), (5, 2, 8, 8200, None), (700, 8, 64, 128, "some")])
+    (33, 32, 40, 72, "some"), (4099, 5, 24, 3400, "some"), (130, 2, 300, 1000, None), (5, 2, 8, 8200, None), (700, 8, 64, 128, "some")])
 def test_dispatch_and_its_gradients(M, L, T, k, E, H, drop, dtype):
     g = gen(T * 31 + H)
     ids = random_ids(g, T, k, E, drop)
