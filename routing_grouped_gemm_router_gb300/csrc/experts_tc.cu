@@ -151,6 +151,15 @@ __device__ __forceinline__ bool mbar_test(uint64_t* b, uint32_t parity) {
   return ok != 0;
 }
 
+// An arrival on CTA `rank`'s barrier that orders none of this thread's own reads and writes. It hands an
+// accumulator back, whose reads tcgen05.wait::ld has seen finished and tcgen05.fence orders; an
+// arrival with release would also wait for the tile's stores to be acknowledged (1650 clocks of the 4200 of
+// a 256 x 256 tile of bf16 dW: 64 experts of 4096 x 2048 over 8 rows each 243 -> 184 us).
+__device__ __forceinline__ void arrive_relaxed(uint64_t* b, uint32_t rank) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr(b, rank))
+               : "memory");
+}
+
 // Thirty-two bytes of a row, to or from global memory: one instruction where `wide` (every row of the
 // matrix starts on a 32-byte boundary), else two. n: 16-byte pieces left of the row's end.
 __device__ __forceinline__ void put32(void* p, const uint32_t (&v)[8], bool wide, int n) {
@@ -367,8 +376,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<KIND, NH>::kT
           uint8_t* a = sA + s * A_BYTES;
           uint8_t* b = sB + s * LY::kStageB;
           if (R::weight) {
-            // the last stage of the reduction: as many 16-row steps as it has (dW of 32 experts of
-            // 5760 x 2880 over 1 to 8 rows each: 298 -> 289 us)
+            // the last stage of the reduction: as many 16-row steps as it has (298 -> 289 us when it came, for
+            // dW of 32 experts of 5760 x 2880 over 1 to 8 rows each, 189 us now)
             const int left = it.cnt - kb * BK, steps = left > 48 ? 4 : (left + 15) / 16;
             if (leader) mbar_expect_tx(&full[s], 2u * (1 + it.nh) * (steps * 4096u));
             const int y = it.row0 + kb * BK, m = it.m0 + (int)rank * 128;
@@ -638,7 +647,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<KIND, NH>::kT
           // dW, often short reductions under large results, where the writes bound: whole 128-byte
           // lines leave through the TMA, which also clips ragged edges and adds to fp32. fp32 dW of 64
           // experts of 4096 x 2048: over 8 rows each 339 us (6.3 TB/s), 444 from registers; over 512 rows
-          // 566 and 582; from 1024 on the two meet.
+          // 566 and 582; from 1024 on the two meet. A second buffer a warp, for a stage of the ring less,
+          // or sixteen warps of one: 355 -> 359 and 361 us over 8 rows, 557 -> 615 and 637 over 512.
           constexpr int W = KIND == kKWeight32 ? 32 : 64;
           uint8_t* const t = smem + LY::out + (size_t)(warp - 2) * OUT_BYTES;
           const int n0 = n * 256;
@@ -729,8 +739,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<KIND, NH>::kT
           tc_fence_before();
           __syncwarp();
           if (lane == 0) {
-            if (leader) mbar_arrive(&tempty[a]);
-            else mbar_arrive_cta(&tempty[a], 0);
+            arrive_relaxed(&tempty[a], 0);
           }
           acc_phase ^= 1u << a;
           if (NH == 1) acc ^= 1;
