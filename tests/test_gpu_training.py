@@ -222,6 +222,13 @@ def test_expert_products_and_gradients(M, L, name, H, I, dtype):
     assert L.moe_device_status(True) == 0
 
 
+# Several rounds of 256-column tiles over the CTA pairs, the last one more or less than half full, with
+# many short runs of rows.
+@pytest.mark.parametrize("H,I", [(264, 520), (520, 264), (1000, 1000)])
+def test_expert_products_over_several_rounds_of_tiles(M, L, H, I):
+    test_expert_products_and_gradients(M, L, "many", H, I, torch.bfloat16)
+
+
 @pytest.mark.parametrize("dtype,out", [(torch.bfloat16, torch.float32), (torch.bfloat16, torch.bfloat16),
                                        (torch.float32, torch.float32)])
 @pytest.mark.parametrize("Mm,N", [(72, 200), (256, 256), (520, 264), (4104, 2600)])
