@@ -20,15 +20,37 @@ from . import _lib as L
 from . import training as ops
 
 
+def _fits(name, t, shape, dtype, device):
+    """ValueError by name unless t is a contiguous tensor of this shape (None: any extent), type and
+    device: the router's entry point takes bare addresses and would misread any other."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name}: a tensor is needed, got {type(t).__name__}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if t.dim() != len(shape) or any(d is not None and d != n for d, n in zip(shape, t.shape)):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected "
+                         f"({', '.join('any' if d is None else str(d) for d in shape)})")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: has to be contiguous (strides {t.stride()})")
+    if t.device != device:
+        raise ValueError(f"{name}: is on {t.device}, expected {device}")
+
+
 class SparseBlock:
-    """Parameters of one block. Wg[E, H], W13[E', 2I, H], W2[E', H, I] in bf16 or fp32 (E' = E +
-    n_shared: shared experts follow the routed ones), gamma_in[H] and gamma_out[H] fp32; gate: None
-    or fp32 [H], the same for all tokens."""
+    """Parameters of one block. Wg[E, H], W13[E', 2I, H], W2[E', H, I] all in bf16 or all in fp32 (E' =
+    E + n_shared: shared experts follow the routed ones), gamma_in[H] and gamma_out[H] fp32; gate: None
+    or fp32 [H], the same for all tokens (where the number of tokens is fixed, any gate of block_join);
+    logit_bias, select_bias: None or fp32 [E]. All contiguous, on one device; anything else raises
+    ValueError."""
 
     def __init__(self, Wg, W13, W2, gamma_in, gamma_out, k: int, gate=None, scale: float = 1.0,
                  mode: int = L.MOE_ROUTE_SOFTMAX, renormalize: bool = True,
                  router_scale: float = 1.0, n_group: int = 1, topk_group: int = 1,
                  logit_bias=None, select_bias=None, n_shared: int = 0, eps: float = 1e-6):
+        if not isinstance(Wg, torch.Tensor) or Wg.dim() != 2 or Wg.dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError("Wg: a bfloat16 or float32 tensor [E, H] is needed")
+        for name, t in (("W13", W13), ("W2", W2)):
+            _fits(name, t, (None, None, None), Wg.dtype, Wg.device)
         if W13.shape[0] != Wg.shape[0] + n_shared or W2.shape[0] != W13.shape[0]:
             raise ValueError(f"W13, W2: {W13.shape[0]} and {W2.shape[0]} experts, expected "
                              f"{Wg.shape[0]} routed and {n_shared} shared ones")
@@ -43,6 +65,27 @@ class SparseBlock:
         self.mode, self.renormalize, self.router_scale = mode, renormalize, router_scale
         self.n_group, self.topk_group = n_group, topk_group
         self.logit_bias, self.select_bias = logit_bias, select_bias
+        self._check_router()
+        for name, t in (("gamma_in", gamma_in), ("gamma_out", gamma_out)):
+            _fits(name, t, (self.H,), torch.float32, Wg.device)
+        if gate is not None:
+            rank = gate.dim() if isinstance(gate, torch.Tensor) else 1
+            full = rank == 2 and gate.shape[1] != 1
+            _fits("gate", gate, (self.H,) if rank == 1 else (None, self.H if full else 1),
+                  Wg.dtype if full else torch.float32, Wg.device)
+
+    def _check_router(self):
+        """What moe_route is given by address besides the tokens."""
+        _fits("Wg", self.Wg, (self.E, self.H), self.W13.dtype, self.W13.device)
+        for name, t in (("logit_bias", self.logit_bias), ("select_bias", self.select_bias)):
+            if t is not None:
+                _fits(name, t, (self.E,), torch.float32, self.Wg.device)
+
+    def _check_tokens(self, name, x):
+        """Token rows that go with the block's weights, on the current CUDA device."""
+        _fits(name, x, (None, self.H), self.Wg.dtype, self.Wg.device)
+        if not x.is_cuda or x.get_device() != torch.cuda.current_device():
+            raise ValueError(f"{name}: is on {x.device}, has to be on the current CUDA device")
 
     def parameters(self):
         """name -> tensor, of those that train."""
@@ -51,6 +94,8 @@ class SparseBlock:
 
     def route(self, h):
         """(logits, topk_ids, topk_w) of ``moe_route``; ids and weights hold k + n_shared slots."""
+        self._check_router()  # attributes can have been replaced
+        self._check_tokens("h", h)
         T, kk = h.shape[0], self.k + self.n_shared
         logits = torch.empty(T, self.E, dtype=torch.float32, device=h.device)
         ids = torch.empty(T, kk, dtype=torch.int32, device=h.device)
@@ -118,6 +163,9 @@ class SparseStack:
         if not blocks:
             raise ValueError("blocks: at least one is needed")
         self.blocks = list(blocks)
+        for i, b in enumerate(self.blocks):  # every block's tokens are the first one's
+            _fits(f"blocks[{i}].Wg", b.Wg, (None, self.blocks[0].H), self.blocks[0].Wg.dtype,
+                  self.blocks[0].Wg.device)
         self.grads = [{n: torch.zeros_like(t, dtype=torch.float32) for n, t in b.parameters().items()}
                       for b in self.blocks]
 
@@ -129,6 +177,7 @@ class SparseStack:
     def forward(self, x):
         """(out[T, H], saved) for x[T, H]."""
         first = self.blocks[0]
+        first._check_tokens("x", x)
         h, rstd = ops.block_norm(x, first.gamma_in, first.eps)
         saved, out = [], x
         for i, b in enumerate(self.blocks):
