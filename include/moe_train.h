@@ -147,7 +147,9 @@ moe_status_t moe_block_norm_backward(const moe_block_t* cfg, const void* dh, con
 
 /* out = x + scale * gate * (y * rstd_y * (offset + gamma)), and with gamma_next the norm before
  * the next block of the same pass: h = out * rstd_out * (offset + gamma_next), read from out as
- * it is stored. gamma_next, h and rstd_out are all given or all NULL. out may be x. */
+ * it is stored. Both norms have cfg's eps and offset; a next norm with others is a moe_block_norm
+ * of out, and moe_block_join_backward takes its rstd as rstd_out. gamma_next, h and rstd_out are
+ * all given or all NULL. out may be x. */
 moe_status_t moe_block_join(const moe_block_t* cfg, const void* x, const void* y,
                             const float* gamma, const void* gate, const float* gamma_next,
                             void* out, float* rstd_y, void* h, float* rstd_out,

@@ -147,7 +147,7 @@ class BlockSaved(NamedTuple):
     y: torch.Tensor
     rstd_y: torch.Tensor
     out: torch.Tensor
-    rstd_out: Optional[torch.Tensor]  # of the next block's norm, taken in the same pass
+    rstd_out: Optional[torch.Tensor]  # of the next block's norm
 
 
 class StackSaved(NamedTuple):
@@ -157,7 +157,8 @@ class StackSaved(NamedTuple):
 
 
 class SparseStack:
-    """Blocks in sequence. A block's residual join also takes the next block's norm."""
+    """Blocks in sequence. A block's residual join also takes the next block's norm, where both blocks
+    have the same eps."""
 
     def __init__(self, blocks: List[SparseBlock]):
         if not blocks:
@@ -182,10 +183,13 @@ class SparseStack:
         saved, out = [], x
         for i, b in enumerate(self.blocks):
             y, s = b.moe(h)
-            nxt = self.blocks[i + 1].gamma_in if i + 1 < len(self.blocks) else None
-            j = ops.block_join(out, y, b.gamma_out, b.gate, b.scale, nxt, b.eps)
-            saved.append(BlockSaved(s, y, j.rstd_y, j.out, j.rstd_out))
-            out, h = j.out, j.h
+            nxt = self.blocks[i + 1] if i + 1 < len(self.blocks) else None
+            fused = nxt is not None and nxt.eps == b.eps  # block_join takes both its norms with one eps
+            j = ops.block_join(out, y, b.gamma_out, b.gate, b.scale, nxt.gamma_in if fused else None, b.eps)
+            out, h, rstd_out = j.out, j.h, j.rstd_out
+            if nxt is not None and not fused:
+                h, rstd_out = ops.block_norm(out, nxt.gamma_in, nxt.eps)
+            saved.append(BlockSaved(s, y, j.rstd_y, out, rstd_out))
         return out, StackSaved(x, rstd, saved)
 
     __call__ = forward

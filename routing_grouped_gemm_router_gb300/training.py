@@ -114,7 +114,8 @@ class Joined(NamedTuple):
 
 def block_join(x, y, gamma, gate=None, scale: float = 1.0, gamma_next=None, eps: float = 1e-6,
                offset: float = 0.0) -> Joined:
-    """out = x + scale * gate * norm(y; gamma), and h = norm(out; gamma_next) of the same pass.
+    """out = x + scale * gate * norm(y; gamma), and h = norm(out; gamma_next) of the same pass, both
+    norms with this eps and offset (a next norm with others: gamma_next None, then block_norm of out).
     gate: None, fp32 [H] (a channel), fp32 [T, 1] (a token) or [T, H] of x's dtype."""
     return Joined._make(C.block_join(x, y, gamma, gate, scale, gamma_next, eps, offset))
 

@@ -99,6 +99,28 @@ def test_gradients_against_autograd(S, dtype, T, kw):
         near(stack.grads[0][name], 2 * t.to(F64), f"twice {name}")
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_every_block_norms_with_its_own_eps(S, dtype):
+    """Blocks of different eps, all of the size of a row's mean square, two of them equal."""
+    stack, rnd = make(S, dtype, seed=3, n=4)
+    for b, eps in zip(stack.blocks, (2.0, 0.25, 0.25, 1e-6)):
+        b.eps = eps
+    x, dout = rnd(37, 136).to(dtype), rnd(37, 136).to(dtype)
+    out, saved = stack.forward(x)
+    dx = stack.backward(dout, saved)
+    blocks64 = [{n: t.to(F64).requires_grad_() for n, t in b.parameters().items()} for b in stack.blocks]
+    x64 = x.to(F64).requires_grad_()
+    ref, loss = reference(stack, saved, x64, dout.to(F64), blocks64)
+    loss.backward()
+    # as for the gradients above: 16 stages a block, each off by its type's half step and fp32's sums
+    tol = 16 * 4 * ((2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -24) + 280 * 2.0 ** -24)
+    pairs = [("out", out, ref.detach()), ("dx", dx, x64.grad)]
+    pairs += [(f"block {i} {n}", g[n], t.grad) for i, (g, p) in enumerate(zip(stack.grads, blocks64))
+              for n, t in p.items()]
+    for what, got, want in pairs:
+        assert (got.to(F64) - want).norm() <= tol * want.norm(), what
+
+
 def test_forward_agrees_with_the_inference_layer(S):
     """y of one block against moe_forward on the same normed input (other kernels, bf16)."""
     from routing_grouped_gemm_router_gb300 import training as ops
