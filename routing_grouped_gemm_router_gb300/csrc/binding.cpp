@@ -11,6 +11,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
@@ -58,8 +59,15 @@ std::string list_of(const R& v) {
 }
 bool is_float(ScalarType t) { return t == ScalarType::BFloat16 || t == ScalarType::Float; }
 
-// A contiguous CUDA tensor of these extents (-1: any), type and device (-1: any). The fast way
-// through is a handful of comparisons; only a tensor that does not fit is described.
+// The calling thread's device, where the library launches: another device's tensors are not this call's.
+int current_device() {
+  c10::DeviceIndex d = -1;
+  return c10::cuda::GetDevice(&d) == cudaSuccess ? d : -1;
+}
+
+// A contiguous CUDA tensor of these extents (-1: any), type and device (-1: the current one, for an
+// operator's first tensor). The fast way through is a handful of comparisons; only a tensor that does
+// not fit is described.
 const Tensor& check(const char* name, PyObject* o, std::initializer_list<int64_t> shape,
                     ScalarType type, int dev) {
   if (!THPVariable_Check(o))
@@ -84,6 +92,9 @@ const Tensor& check(const char* name, PyObject* o, std::initializer_list<int64_t
   if (!t.is_cuda()) throw Refused{std::string(name) + ": has to be on a CUDA device"};
   if (dev >= 0 && t.get_device() != dev)
     throw Refused{std::string(name) + ": is on another device than the other tensors"};
+  if (dev < 0 && t.get_device() != current_device())
+    throw Refused{std::string(name) + ": is on cuda:" + std::to_string(t.get_device()) +
+                  ", which is not the current device"};
   return t;
 }
 

@@ -164,6 +164,38 @@ def test_wrappers_refuse_wrong_tensors(M):
             fn()
 
 
+def calls_on(M, dev):
+    """A call of every operator whose tensors, none of which has memory, lie on `dev`."""
+    f, bf, i32 = torch.float32, torch.bfloat16, torch.int32
+    t = lambda *s, dtype=bf: torch.zeros(*s, dtype=dtype, device=dev)  # noqa: E731
+    T, k, E, H, I, P = 4, 2, 8, 64, 48, 128
+    x, ids, w = t(T, H), t(T, k, dtype=i32), t(T, k, dtype=f)
+    rows, sid, cnt = t(P, H), t(P, dtype=i32), t(E, dtype=i32)
+    W13, W2, act, h13, dh13 = t(E, 2 * I, H), t(E, H, I), t(P, I), t(P, 2 * I, dtype=f), t(P, 2 * I)
+    g, r, logits = t(H, dtype=f), t(T, dtype=f), t(T, E, dtype=f)
+    return {
+        "topk_ids": lambda: M.sort_tokens(ids, E), "x": lambda: M.permute(x, ids, sid, E),
+        "dxs": lambda: M.permute_backward(rows, ids), "ys": lambda: M.unpermute(rows, ids, w),
+        "ys ": lambda: M.unpermute_backward(x, rows, sid, ids, w), "xs": lambda: M.expert_up(rows, W13, cnt),
+        "act": lambda: M.expert_down(act, W2, cnt), "dys": lambda: M.expert_down_backward(rows, W2, h13, cnt),
+        "dh13": lambda: M.expert_up_backward(dh13, W13, cnt), "dy": lambda: M.expert_weight_grad(rows, act, cnt),
+        "x ": lambda: M.block_norm(x, g), "x  ": lambda: M.block_norm_backward(x, x, g, r),
+        "x   ": lambda: M.block_join(x, x, g), "y": lambda: M.block_join_backward(x, x, g, r),
+        "logits": lambda: M.route_backward(logits, ids, w)}
+
+
+def test_wrappers_refuse_tensors_of_a_device_that_is_not_current(M):
+    """Kernels start on the calling thread's device, whatever device a tensor's addresses belong to."""
+    from torch._subclasses.fake_tensor import FakeTensorMode
+    from routing_grouped_gemm_router_gb300 import _native
+    with FakeTensorMode():
+        calls = calls_on(M, "cuda:1")
+    assert len(calls) == len([n for n in dir(_native) if not n.startswith("__") and n != "set_error"])
+    for name, fn in calls.items():
+        with pytest.raises(ValueError, match=f"^{name.strip()}: is on cuda:1, which is not the current device"):
+            fn()
+
+
 def test_buffer_rows(M):
     assert M.buffer_rows(1, 1, 1) == 16
     assert M.buffer_rows(4096, 8, 256) == (4096 * 8 + 256 * 15) // 16 * 16
