@@ -662,6 +662,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<KIND, NH>::kT
 #pragma unroll
             for (int x = 0; x < W; x += 32) {
               uint32_t v[32];
+              __syncwarp();  // the aligned load below: the lanes part where some add old values
               if (computed) {
                 tmem_ld32(tb + c + x, v);
                 tmem_ld_wait();
