@@ -758,6 +758,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<KIND, NH>::kT
     const uint64_t t0 = gtimer();
     while (gtimer() - t0 < 200000ull) {
     }
+    __syncwarp();  // the clock lets lanes go one by one; what follows takes whole warps
   }
   cluster_sync();  // no remote arrival still targets this CTA; both CTAs are done with TMEM
   if (warp == 1) {

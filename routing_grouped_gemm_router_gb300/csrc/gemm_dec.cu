@@ -514,6 +514,7 @@ __global__ void __launch_bounds__(Cfg<MODE, FP8>::kThreads, 1)
     const uint64_t t0 = gtimer();
     while (gtimer() - t0 < 200000ull) {
     }
+    __syncwarp();  // the clock lets lanes go one by one; what follows takes whole warps
   }
   if (warp == 1) {
     tc_fence_after();
