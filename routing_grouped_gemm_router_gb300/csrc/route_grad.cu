@@ -71,7 +71,11 @@ __global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(
     dot = warp_total(g * p);
     grad = scale * p * (g - dot);
   } else {
-    const float s = id >= 0 ? 1.f / (1.f + expf(-z)) : 0.f;
+    // s and 1 - s each from the smaller exponential: taken from a rounded s, 1 - s would be off by
+    // a thousandth of itself at z = 10 and zero from z = 17 on
+    const float x = id >= 0 ? expf(-fabsf(z)) : 0.f;
+    const float large = 1.f / (1.f + x), small = x * large;
+    const float s = id >= 0 ? (z >= 0.f ? large : small) : 0.f, r = z >= 0.f ? small : large;
     float ds = g;
     if (renorm) {
       const float sum = warp_total(s);
@@ -79,7 +83,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(
       dot = warp_total(g * q);
       ds = id >= 0 ? (g - dot) / sum : 0.f;
     }
-    grad = scale * ds * s * (1.f - s);
+    grad = scale * ds * s * r;
   }
 
   float d[MPL];

@@ -30,3 +30,47 @@ def test_bf16_weight_gradients_added_to_by_part_of_a_warp(M, Mm, N):
         d, v = dy[r].to(F64), a[r].to(F64)
         mag = d.abs().T @ v.abs() + before[e].to(F64).abs()
         within(dW[e], before[e].to(F64) + d.T @ v, (r.stop - r.start + 3) * U * mag, BF, f"expert {e}")
+
+
+def test_fp32_weight_gradients_keep_values_below_the_normal_range(M):
+    """Sums and old values under 2^-126 are neither flushed on the way out nor by the addition, whether
+    the tile leaves through the copy engine or from registers, in any of the kernels."""
+    for dtype, Mm, N, rows in ((BF, 64, 64, 16), (F32, 64, 64, 16), (BF, 4104, 2600, 5200)):
+        cnt = torch.tensor([rows], dtype=torch.int32, device=DEV)
+        dy, a = torch.zeros(rows, Mm, dtype=dtype, device=DEV), torch.zeros(rows, N, dtype=dtype, device=DEV)
+        dW = torch.full((1, Mm, N), 2.0 ** -133, device=DEV)
+        M.expert_weight_grad(dy, a, cnt, out=dW, accumulate=True)
+        assert (dW == 2.0 ** -133).all()
+        dy[0], a[0] = 2.0 ** -70, 2.0 ** -62
+        assert (M.expert_weight_grad(dy, a, cnt, out_dtype=F32) == 2.0 ** -132).all()
+        dy[0], a[0] = 2.0 ** -60, 2.0 ** -66
+        dW.fill_(-1.5 * 2.0 ** -126)
+        M.expert_weight_grad(dy, a, cnt, out=dW, accumulate=True)
+        assert (dW == -0.5 * 2.0 ** -126).all()
+
+
+@pytest.mark.parametrize("k", [1, 3, 8])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_sigmoid_router_gradient_of_large_logits(M, k, renorm):
+    """s (1 - s) where s is next to one: the difference may not be taken from the rounded s."""
+    steps = torch.tensor([-30.0, -17.0, -8.0, -1.0, 0.0, 1.0, 8.0, 17.0, 30.0], device=DEV)
+    E, T = 16, 64
+    g = gen(k)
+    logits = steps[torch.randint(len(steps), (T, E), generator=g, device=DEV)] + 0.5 * randn(g, T, E)
+    logits[:len(steps)] = steps[:, None]  # and rows of equal ones
+    ids = torch.rand(T, E, generator=g, device=DEV).topk(k, dim=1).indices
+    dw = randn(g, T, k)
+    z, d64 = logits.to(F64).gather(1, ids), dw.to(F64)
+    s = torch.sigmoid(z)
+    slope = s * torch.sigmoid(-z)
+    S = s.sum(1, keepdim=True)
+    want = 1.5 * slope * ((d64 - (d64 * s / S).sum(1, keepdim=True)) / S if renorm else d64)
+    got = M.route_backward(logits, ids.to(torch.int32), dw, mode=1, renormalize=renorm, scale=1.5)
+    # expf of an exact argument: 2 units, 4 half ones; one sum, one divide a factor; three products: 16 half units
+    # with room. Renormalised, k-term sums and the quotient s / S add k + 14, to a difference of at most 2 amp
+    # (relative) and to its subtrahend of at most amp: 3 k + 48
+    amp = d64.abs().max(1, keepdim=True).values
+    slack = 1.5 * slope * ((3 * k + 48) * U * amp / S if renorm else 16 * U * d64.abs())
+    within(got.gather(1, ids), want, slack, F32, "dlogits")
+    rest = torch.ones(T, E, dtype=torch.bool, device=DEV).scatter_(1, ids, False)
+    assert (got[rest] == 0).all()
