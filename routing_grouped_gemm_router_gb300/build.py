@@ -3,8 +3,8 @@ CPython extension that calls its training operators on torch tensors (host compi
 
 ``python -m routing_grouped_gemm_router_gb300.build`` (or ``build()``) writes
 ``libmoe_gb300.so`` and ``_native.so`` next to this file. Objects go to ``_build/`` in the package
-directory. Sources are compiled in parallel; up-to-date libraries are not rebuilt. Without
-PyTorch the extension is left out: the C ABI does not need it.
+directory. Sources are compiled in parallel; up-to-date libraries are not rebuilt. Without a
+PyTorch that has CUDA libraries the extension is left out: the C ABI does not need it.
 """
 from __future__ import annotations
 
@@ -46,8 +46,10 @@ def _deps():
 
 
 def _torch_dir():
+    """Where PyTorch is installed; None without one that has CUDA libraries."""
     spec = importlib.util.find_spec("torch")
-    return os.path.dirname(spec.origin) if spec and spec.origin else None
+    d = os.path.dirname(spec.origin) if spec and spec.origin else None
+    return d if d and os.path.exists(os.path.join(d, "lib", "libc10_cuda.so")) else None
 
 
 def _native_up_to_date() -> bool:

@@ -1,0 +1,28 @@
+"""When the build compiles the extension of the training operators, and when it leaves it out."""
+import importlib.util
+import os
+import types
+
+import pytest
+
+from conftest import ROOT
+
+
+@pytest.fixture
+def B():
+    path = os.path.join(ROOT, "routing_grouped_gemm_router_gb300", "build.py")
+    spec = importlib.util.spec_from_file_location("_build_under_test", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    return mod
+
+
+def test_the_extension_is_left_out_without_pytorch_s_cuda_libraries(B, monkeypatch, tmp_path):
+    (tmp_path / "lib").mkdir()
+    spec = types.SimpleNamespace(origin=str(tmp_path / "__init__.py"))
+    monkeypatch.setattr(B.importlib.util, "find_spec", lambda name: spec)
+    assert B._torch_dir() is None and B._native_up_to_date()
+    (tmp_path / "lib" / "libc10_cuda.so").touch()
+    assert B._torch_dir() == str(tmp_path)
+    monkeypatch.setattr(B.importlib.util, "find_spec", lambda name: None)
+    assert B._torch_dir() is None
