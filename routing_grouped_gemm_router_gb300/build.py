@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.metadata
 import importlib.util
 import os
 import shutil
@@ -24,6 +25,7 @@ OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe_gb300.so")
 BINDING = os.path.join(CSRC, "binding.cpp")
 NATIVE = os.path.join(PKG, "_native.so")
+NATIVE_FOR = os.path.join(OBJ, "native_for.txt")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE,
@@ -52,9 +54,20 @@ def _torch_dir():
     return d if d and os.path.exists(os.path.join(d, "lib", "libc10_cuda.so")) else None
 
 
+def _native_for() -> str:
+    """The Python and the PyTorch that an extension compiled now is for: it fits no other."""
+    try:
+        torch_version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        torch_version = "of unknown version"
+    return f"{sys.version} torch {torch_version} {_torch_dir()}"
+
+
 def _native_up_to_date() -> bool:
     if _torch_dir() is None:
         return True
+    if not os.path.exists(NATIVE_FOR) or open(NATIVE_FOR).read() != _native_for():
+        return False
     return os.path.exists(NATIVE) and all(
         os.path.getmtime(d) <= os.path.getmtime(NATIVE)
         for d in [BINDING, __file__, *glob.glob(os.path.join(INCLUDE, "*.h"))])
@@ -85,6 +98,8 @@ def _link_binding(obj):
     if r.returncode != 0:
         raise RuntimeError(f"link of the extension failed:\n{r.stderr}")
     os.replace(tmp, NATIVE)
+    with open(NATIVE_FOR, "w") as f:
+        f.write(_native_for())
 
 
 def up_to_date() -> bool:

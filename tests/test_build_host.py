@@ -26,3 +26,22 @@ def test_the_extension_is_left_out_without_pytorch_s_cuda_libraries(B, monkeypat
     assert B._torch_dir() == str(tmp_path)
     monkeypatch.setattr(B.importlib.util, "find_spec", lambda name: None)
     assert B._torch_dir() is None
+
+
+def test_an_extension_for_another_python_or_pytorch_is_built_again(B, monkeypatch, tmp_path):
+    if B._torch_dir() is None:
+        pytest.skip("no PyTorch with CUDA libraries")
+    native, mark = tmp_path / "_native.so", tmp_path / "native_for.txt"
+    native.touch()  # newer than every source
+    monkeypatch.setattr(B, "NATIVE", str(native))
+    monkeypatch.setattr(B, "NATIVE_FOR", str(mark), raising=False)
+    assert not B._native_up_to_date()  # not known what it is for
+    mark.write_text(B._native_for())
+    assert B._native_up_to_date()
+    monkeypatch.setattr(B.importlib.metadata, "version", lambda name: "2.0.0")
+    assert not B._native_up_to_date()
+    monkeypatch.undo()
+    monkeypatch.setattr(B, "NATIVE", str(native))
+    monkeypatch.setattr(B, "NATIVE_FOR", str(mark))
+    monkeypatch.setattr(B.sys, "version", "3.9.0")
+    assert not B._native_up_to_date()
