@@ -74,3 +74,38 @@ def test_sigmoid_router_gradient_of_large_logits(M, k, renorm):
     within(got.gather(1, ids), want, slack, F32, "dlogits")
     rest = torch.ones(T, E, dtype=torch.bool, device=DEV).scatter_(1, ids, False)
     assert (got[rest] == 0).all()
+
+
+# Rows enough for five to dozens of units of rows a CTA, the last one ragged: stages of the ring are filled
+# again and their order wraps, scalars are asked for a row ahead, column sums run over many units. Short rows
+# have eight in a unit (65,541 of them: at most 8 CTAs an SM), 8200 channels of fp32 and 20,000 have no ring.
+LONG = [(64, 65541), (264, 40003), (2880, 8195), (4096, 8195), (8200, 2051), (20000, 1027)]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("kind", ["none", "channel", "token", "full"])
+@pytest.mark.parametrize("H,T", LONG)
+def test_join_and_its_gradient_over_long_batches(M, H, T, kind, dtype):
+    join_and_its_gradient(M, H, T, kind, dtype)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("H,T", LONG)
+def test_norm_and_its_gradient_over_long_batches(M, H, T, dtype):
+    g, eps = gen(H + T), 1e-6
+    for offset, with_res in ((0.0, True), (1.0, False)):
+        x, dh, dres = (randn(g, T, H, dtype=dtype, std=2.0) for _ in range(3))
+        gamma = 1 - offset + randn(g, H, std=0.3)
+        h, r = M.block_norm(x, gamma, eps=eps, offset=offset)
+        x64, gm, gmm, d64 = x.to(F64), offset + gamma.to(F64), offset + gamma.to(F64).abs(), dh.to(F64)
+        r64 = (x64 * x64).mean(1, keepdim=True).add(eps).rsqrt()
+        rel = (H / 2 + 8) * U
+        within(r, r64[:, 0], rel * r64[:, 0], F32, "rstd")
+        within(h, x64 * r64 * gm, (rel + 3 * U) * (x64 * r64).abs() * gmm, dtype, "h")
+        dx, dg = M.block_norm_backward(dh, x, gamma, r, dres=dres if with_res else None, offset=offset)
+        rk = r.to(F64)[:, None]
+        a, am, xn = d64 * gm, d64.abs() * gmm, x64 * rk
+        res = dres.to(F64) if with_res else torch.zeros_like(x64)
+        slack = (H + 8) * U * rk * (am + xn.abs() * (am * xn.abs()).mean(1, keepdim=True)) + 2 * U * res.abs()
+        within(dx, rk * (a - xn * (a * xn).mean(1, keepdim=True)) + res, slack, dtype, "dx")
+        within(dg, (d64 * xn).sum(0), (T + 4) * U * (d64 * xn).abs().sum(0), F32, "dgamma")
