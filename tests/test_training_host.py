@@ -184,11 +184,12 @@ def calls_on(M, dev):
         "logits": lambda: M.route_backward(logits, ids, w)}
 
 
-def test_wrappers_refuse_tensors_of_a_device_that_is_not_current(M):
+def test_wrappers_refuse_tensors_of_a_device_that_is_not_current(M, monkeypatch):
     """Kernels start on the calling thread's device, whatever device a tensor's addresses belong to."""
     from torch._subclasses.fake_tensor import FakeTensorMode
     from routing_grouped_gemm_router_gb300 import _native
-    with FakeTensorMode():
+    with monkeypatch.context() as m, FakeTensorMode():
+        m.setattr(torch.cuda, "is_available", lambda: False)  # no second GPU is touched to describe it
         calls = calls_on(M, "cuda:1")
     assert len(calls) == len([n for n in dir(_native) if not n.startswith("__") and n != "set_error"])
     for name, fn in calls.items():
