@@ -57,8 +57,11 @@ __global__ void __launch_bounds__(256) permute_kernel(const uint4* __restrict__ 
 // Where the copies outgrow L2, token rows would come from HBM several times that way (199 MB read for
 // 58 MB of tokens: 114 us for 4096 x 7168 with 8 slots each). So positions are written first, by a
 // kernel of their own, and then a thread reads a 16-byte piece of a token once and writes it to the
-// token's k rows: 89 us, 5.9 TB/s written. The first blocks write the rows of no slot.
-constexpr size_t kTokenMajorFrom = (size_t)1 << 27;  // bytes of xs; below, one kernel is quicker
+// token's k rows: 89 us, 5.9 TB/s written. The first blocks write the rows of no slot. Row-major against
+// token-major over 64 experts, us, 2048 and 7168 channels: xs of 64 MB 13 to 16 and 12 to 22, 128 MB 27 to 39
+// and 25 to 33, 256 MB 56 to 79 and 49 to 62, 512 MB 125 to 165 and 94 to 121 (2, 4 and 8 slots a token). With
+// one slot nothing is read twice: 43 and 44 us at 128 MB, 167 and 169 at 512.
+constexpr size_t kTokenMajorFrom = (size_t)1 << 27;  // bytes of xs, for two slots a token or more
 constexpr int kZeroRows = 64;                        // table entries a zeroing block looks at
 
 __global__ void __launch_bounds__(256) positions_kernel(const int32_t* __restrict__ ids,
@@ -235,7 +238,7 @@ moe_status_t launch_permute(const void* x, const int32_t* ids, const int32_t* si
   const int threads = vec >= 256 ? 256 : std::max(32, ceil_div(vec, 32) * 32);
   const int parts = ceil_div(vec, threads);
   const int64_t grid = (int64_t)T * parts + ceil_div(rows, kZeroRows);
-  if ((size_t)rows * vec * 16 >= kTokenMajorFrom && grid <= 0x7fffffff) {
+  if (k > 1 && (size_t)rows * vec * 16 >= kTokenMajorFrom && grid <= 0x7fffffff) {
     const int blocks = std::min(ceil_div(std::max(rows, T * k), 256), num_sms() * 4);
     const moe_status_t st = launch_k(positions_kernel, dim3(blocks), dim3(256), 0, s, ids, sid, T * k, E,
                                      rows, pos);

@@ -109,3 +109,21 @@ def test_norm_and_its_gradient_over_long_batches(M, H, T, dtype):
         slack = (H + 8) * U * rk * (am + xn.abs() * (am * xn.abs()).mean(1, keepdim=True)) + 2 * U * res.abs()
         within(dx, rk * (a - xn * (a * xn).mean(1, keepdim=True)) + res, slack, dtype, "dx")
         within(dg, (d64 * xn).sum(0), (T + 4) * U * (d64 * xn).abs().sum(0), F32, "dgamma")
+
+
+@pytest.mark.parametrize("k", [1, 2])
+def test_permute_of_copies_past_l2(M, L, k):
+    """160 MB of copies: a token's row is read once for all of its slots, or, with one slot, row by row."""
+    T, E, H = 20000 // k, 24, 4096
+    g = gen(k)
+    ids = torch.rand(T, E, generator=g, device=DEV).topk(k, dim=1).indices.to(torch.int32)
+    ids[::7, 0] = -1
+    x = randn(g, T, H, dtype=BF)
+    sid = M.sort_tokens(ids, E).sorted_ids
+    xs, pos = M.permute(x, ids, sid, E)
+    live = sid < T * k
+    assert torch.equal(xs[live], x[sid[live].long() // k]) and (xs[~live] == 0).all()
+    want = torch.full((T * k,), -1, dtype=torch.int32, device=DEV)
+    want[sid[live].long()] = torch.arange(len(sid), dtype=torch.int32, device=DEV)[live]
+    assert torch.equal(pos.view(-1), want)
+    assert L.moe_device_status(True) == 1  # the dropped slots
