@@ -12,7 +12,7 @@
 // consecutive rows at a time (R > 1 where rows are short), a group of threads a row; each thread
 // copies the pieces of its next rows into shared memory asynchronously (cp.async, its own pieces
 // alone, so no barrier guards them) while it works on the current row from registers, so loads are
-// in flight through the two reductions that a row has to wait for. Sums are fp32. Column sums over
+// in flight through the reductions that a row has to wait for. Sums are fp32. Column sums over
 // tokens (the weights' and a shared channel gate's gradients) stay in registers over all of a
 // thread's rows, are added over the CTA's groups, written as one partial row a CTA, and added by a
 // second kernel in a fixed order: no atomics, the same bits every run.
@@ -27,26 +27,15 @@ using namespace ptx;
 constexpr int kMaxIn = 5;         // row tensors a kernel reads
 constexpr int kMaxStages = 3;
 constexpr int kMaxThreads = 512;  // of a CTA
-// Threads of an instance's CTA at most: 448 leave the backward kernels 146 registers.
+// Threads of an instance's CTA at most: 448 leave the backward kernels 144 registers.
 template <int VPT>
 constexpr int kThreadsOf = VPT == 2 ? 448 : kMaxThreads;
 constexpr int kRingBudget = 128 * 1024;  // bytes of rows in flight an SM; the rest is L1 (the weights)
 
-// Two fp32 values that one instruction works on: the arithmetic of a row, not only its bytes, has
-// to fit in the time HBM leaves (an element passes through about 20 operations forward and 30
-// backward), and packed operations halve it.
-struct F2 {
-  uint64_t v;
-};
-__device__ __forceinline__ F2 f2(float lo, float hi) {
-  F2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
-  return r;
-}
+// Packed pairs (F2): the arithmetic of a row, not only its bytes, has to fit in the time HBM leaves
+// (an element passes through about 20 operations forward and 30 backward), and packed operations
+// halve it.
 __device__ __forceinline__ F2 dup(float s) { return f2(s, s); }
-__device__ __forceinline__ void split(F2 a, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a.v));
-}
 __device__ __forceinline__ F2 operator*(F2 a, F2 b) {
   F2 r;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
@@ -55,11 +44,6 @@ __device__ __forceinline__ F2 operator*(F2 a, F2 b) {
 __device__ __forceinline__ F2 operator+(F2 a, F2 b) {
   F2 r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-  F2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
   return r;
 }
 __device__ __forceinline__ float both(F2 a) {
@@ -140,7 +124,6 @@ __device__ __forceinline__ void load_w(const float* p, int i, F2 (&f)[4]) {
 struct Shape {
   int T, H, chunks, group, per, units;
   float scale, offset, eps, inv_h;
-  int gate;
   int n_in;           // row tensors read
   int stages;
   const void* in[kMaxIn];
@@ -580,7 +563,6 @@ static Shape shape_of(const moe_block_t& c, bool join) {
   s.offset = c.offset;
   s.eps = c.eps;
   s.inv_h = 1.0f / (float)c.H;
-  s.gate = c.gate_kind;
   return s;
 }
 

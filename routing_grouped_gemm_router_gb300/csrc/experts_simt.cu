@@ -59,45 +59,23 @@ struct Tile {
   }
 };
 
-// Two fp32 sums that one instruction advances.
-struct F2 {
-  uint64_t v;
-};
-__device__ __forceinline__ F2 f2(float lo, float hi) {
-  F2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ void split(F2 a, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a.v));
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-  F2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return r;
-}
-
 // acc[i][j] += sum over a tile's 16 steps of rows ty * MR + 2i, + 1 of a times column j of this
 // thread. Its eight columns are tx * 4 .. + 3 and 64 + tx * 4 .. + 3. Pairs of rows share an
 // instruction, which leaves issue slots for everything else.
 template <int MR, int TM>
 __device__ __forceinline__ void multiply(const float (*a)[TM + PAD], const float (*b)[TN + PAD],
                                          F2 (&acc)[MR / 2][8]) {
+  static_assert(MR % 4 == 0, "whole pieces of a column");
   const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
 #pragma unroll
   for (int k = 0; k < TK; ++k) {
     F2 x[MR / 2];
     float y[8];
-    if constexpr (MR % 4 == 0) {
 #pragma unroll
-      for (int i = 0; i < MR; i += 4) {
-        const float4 q = *(const float4*)&a[k][ty * MR + i];
-        x[i / 2] = f2(q.x, q.y);
-        x[i / 2 + 1] = f2(q.z, q.w);
-      }
-    } else {
-      const float2 q = *(const float2*)&a[k][ty * MR];
-      x[0] = f2(q.x, q.y);
+    for (int i = 0; i < MR; i += 4) {
+      const float4 q = *(const float4*)&a[k][ty * MR + i];
+      x[i / 2] = f2(q.x, q.y);
+      x[i / 2 + 1] = f2(q.z, q.w);
     }
     *(float4*)&y[0] = *(const float4*)&b[k][tx * 4];
     *(float4*)&y[4] = *(const float4*)&b[k][64 + tx * 4];

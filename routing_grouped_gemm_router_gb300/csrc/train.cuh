@@ -50,6 +50,25 @@ __device__ __forceinline__ float warp_total(float v) {
   return v;
 }
 
+// ------------------------------------------------------------------- packed fp32
+// Two fp32 values that one instruction works on.
+struct F2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void split(F2 a, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a.v));
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+
 // ------------------------------------------------------------------- experts' rows
 constexpr int kRowBlock = MOE_TRAIN_BLOCK;
 constexpr int kMaxExperts = 512;
