@@ -126,6 +126,8 @@ class SparseBlock:
         dlogits = ops.route_backward(s.logits, s.topk_ids, dw, self.mode, self.renormalize,
                                      self.router_scale, self.logit_bias, self.n_shared)
         grads["Wg"].addmm_(dlogits.T, s.h.float())
+        # with bf16 weights dlogits is rounded to bf16 here, as the product of two bf16 matrices takes it:
+        # each term is then off by at most 2^-8 of itself, as h and Wg are, and the sum over experts is fp32
         return torch.addmm(dh, dlogits.to(dh.dtype), self.Wg)
 
 
