@@ -544,8 +544,9 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(const float* __restric
 
 // Chunks of 8 elements a thread holds. More of them share the fixed cost of a warp's row (the
 // reductions), until registers run out: the join's kernels hold four rows and their sums. Measured at
-// 8192 rows of bf16, two against four chunks: join of 4096 channels 55 and 61 us, its gradient 92 and
-// 119; norm of 7168 channels 51 and 43.
+// 8192 rows of bf16, two against four chunks, us: join of 4096 channels 51 and 60, its gradient 84 and
+// 119; of 7168 channels 90 and 98, 146 and 193. Norm of 5120 channels 35.3 and 34.7, its gradient 67 and 70;
+// of 7168 50 and 54, 103 and 93: one rule for both directions, for the gradient's sake.
 static int vec_of(const moe_block_t& c, bool join) {
   const int chunks = c.H / 8;
   const int two = join || c.dtype == MOE_F32 ? 896 : 512;

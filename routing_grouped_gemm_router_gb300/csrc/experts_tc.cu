@@ -22,6 +22,11 @@
 // items on and off, whether the TMA or the threads stored them. (The weight gradients' narrow form,
 // whose reductions are short and results large, is the exception: see there.)
 //
+// The accumulators cut sums off where fp32 arithmetic rounds: the error is toward zero and grows with the
+// length of a reduction, 1.1e-9 of a result's size a step (weight gradients of random rows: 4.7e-7 over 512 rows,
+// 2.1e-6 over 2048, 9.1e-6 over 8192, the same as the library's bf16 product with fp32 results). bf16 results,
+// off by 1.7e-3 from their rounding, do not show it.
+//
 // Roles in each CTA of a pair: warp 0 issues the TMA loads into a ring of stages, warp 1 of the
 // leader issues the MMAs, the others are the epilogue. Tensor memory holds two 256-column
 // accumulators. Work items are (expert, 256-row tile, NH 256-column tiles), weight panels outermost
