@@ -106,9 +106,8 @@ moe_status_t moe_expert_up_backward(const moe_experts_t* cfg, const void* dh13, 
  * W2's gradient takes dy = dys, a = act (M = H, N = I), W13's dy = dh13, a = xs (M = 2I,
  * N = H). dtype is that of dy and a; out_dtype (MOE_F32, or MOE_BF16 when dtype is) that of
  * dW. accumulate 0: dW is overwritten (zeros for an expert without rows); 1: added to, the sum
- * rounded once. From bf16 rows dW_e carries the tensor cores' accumulation, which cuts off rather than
- * rounds: measured 1.1e-9 of its size a row (9.1e-6 over 8192 rows), toward zero; calls over fewer rows each,
- * accumulated, keep fp32 gradients closer. From fp32 rows sums are rounded fp32. */
+ * rounded once. The tensor cores' accumulators cut off rather than round; fp32 dW of bf16 rows leaves them
+ * every 512 rows and is added up in rounded fp32 (off by 4.8e-7 of its size over 512 to 8192 rows). */
 moe_status_t moe_expert_weight_grad(int rows, int E, int M, int N, moe_dtype_t dtype,
                                     moe_dtype_t out_dtype, int accumulate, const void* dy,
                                     const void* a, const int32_t* counts, void* dW,

@@ -23,9 +23,12 @@
 // whose reductions are short and results large, is the exception: see there.)
 //
 // The accumulators cut sums off where fp32 arithmetic rounds: the error is toward zero and grows with the
-// length of a reduction, 1.1e-9 of a result's size a step (weight gradients of random rows: 4.7e-7 over 512 rows,
-// 2.1e-6 over 2048, 9.1e-6 over 8192, the same as the library's bf16 product with fp32 results). bf16 results,
-// off by 1.7e-3 from their rounding, do not show it.
+// length of a reduction (weight gradients of random rows: 4.7e-7 of their size over 512 rows, 2.1e-6 over 2048,
+// 9.1e-6 over 8192, the same as in the library's bf16 product with fp32 results). bf16 results, off by 1.7e-3
+// from their rounding, do not show it. fp32 weight gradients leave the accumulators every 512 rows and are
+// added up in registers: 4.8e-7 over 8192 rows. That takes 2 to 3 % at up to 1000 rows an expert, 5 % at
+// 2048, 7 % at 4096, and the wide form (below), whose two tiles would be 256 sums a thread: with it, 2 experts of
+// 4096 x 4096 over 8192 rows took 343 us, without 387.
 //
 // Roles in each CTA of a pair: warp 0 issues the TMA loads into a ring of stages, warp 1 of the
 // leader issues the MMAs, the others are the epilogue. Tensor memory holds two 256-column
@@ -59,12 +62,14 @@ constexpr int B_BYTES = 128 * 128;   // of one 256-column tile
 constexpr int CHUNK = 64 * 128;      // one 64-column box of an M/N-major operand: 64 K rows x 128 B
 
 constexpr int OUT_BYTES = 32 * 128;  // a staged tile of dW: 32 rows of 128 bytes
+constexpr int kSplit = 8;            // stages (of BK rows) of an fp32 dW that the accumulators add up
 
 template <int KIND>
 struct Traits {
   static constexpr bool weight = KIND >= kKWeight32;
   static constexpr bool a_mn = weight;  // operand contiguous along M rather than K
   static constexpr bool b_mn = KIND >= kKDownGrad;
+  static constexpr bool split = KIND == kKWeight32;  // sums leave the accumulators every kSplit stages
   static constexpr uint32_t idesc =
       idesc_bf16(256, 256) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
 };
@@ -446,8 +451,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<KIND, NH>::kT
           tc_fence_after();
           return true;
         };
-        // stage kb into accumulator a, B tile h
-        auto mma = [&](int kb, int h, int a) {
+        // stage kb into accumulator a, B tile h; stage `first` overwrites it
+        auto mma = [&](int kb, int h, int a, int first = 0) {
           const int s = (g0 + kb) % kStages;
           const uint32_t sa = su32(sA + s * A_BYTES), sb = su32(sB + s * LY::kStageB + h * B_BYTES);
           const uint32_t d = tmem_base + (uint32_t)(a * 256);
@@ -457,7 +462,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<KIND, NH>::kT
             if (kk < steps)
               umma_bf16<2>(d, R::a_mn ? mn_desc(sa + kk * 2048) : sw128_desc(sa + kk * 32),
                            R::b_mn ? mn_desc(sb + kk * 2048) : sw128_desc(sb + kk * 32), R::idesc,
-                           (kb | kk) != 0 ? 1u : 0u);
+                           ((kb - first) | kk) != 0 ? 1u : 0u);
           }
           issued = true;
         };
@@ -467,7 +472,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<KIND, NH>::kT
           tc_fence_after();
           return *abort_flag == 0;
         };
-        if (NH == 1 || it.nh == 1) {
+        if constexpr (R::split) {
+          for (int k0 = 0; k0 < T && ok; k0 += kSplit) {
+            const int a = acc, k1 = min(T, k0 + kSplit);
+            if (!(ok = acc_free(a))) break;
+            for (int kb = k0; kb < k1; ++kb) {
+              if (!(ok = wait_full(kb))) break;
+              mma(kb, 0, a, k0);
+              release(kb);
+            }
+            if (!ok) break;
+            umma_commit_pair(&tfull[a], 0x3);
+            acc_phase ^= 1u << a;
+            acc ^= 1;
+          }
+          if (!ok) break;
+        } else if (NH == 1 || it.nh == 1) {
           const int a = NH == 1 ? acc : 0;
           if (!acc_free(a)) break;
           for (int kb = 0; kb < T && ok; ++kb) {
@@ -556,7 +576,86 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<KIND, NH>::kT
       uint8_t* const act = (uint8_t*)P.act + (int64_t)(m + lane) * P.act_bytes;
       const float* const hrow = P.h13 + (int64_t)(m + lane) * 2 * P.N;
       const bool wide = P.wide;
-      for (int h = 0; h < it.nh; ++h) {
+      if constexpr (R::split) {
+        // fp32 dW: the sums of kSplit stages at a time are added up in registers; the last ones are added on
+        // their way out, as whole 128-byte lines through the TMA, which also clips ragged edges and adds to
+        // fp32. dW of 64 experts of 4096 x 2048 over 8 rows each took 339 us (6.3 TB/s) so, 444 in stores from
+        // registers; a second buffer a warp, for a stage of the ring less, or sixteen warps of one 359 and 361.
+        float sum[kCols] = {};
+        const int n0 = it.n * 256 + part * kCols;
+        const int segs = (it.num_kb + kSplit - 1) / kSplit;
+        uint8_t* const t = smem + LY::out + (size_t)(warp - 2) * OUT_BYTES;
+        uint32_t tb = 0;
+#pragma unroll 1
+        for (int g = 0; g < segs; ++g) {
+          int ok = 1;
+          if (lane == 0) ok = wait_bounded_inline(&tfull[acc], (acc_phase >> acc) & 1u, abort_flag, status);
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          if (!ok) {
+            ok_all = false;
+            break;
+          }
+          tc_fence_after();
+          tb = tmem_base + (uint32_t)(acc * 256 + part * kCols) + ((uint32_t)(q * 32) << 16);
+          if (g == segs - 1) break;
+          if (m < end) {
+#pragma unroll
+            for (int c = 0; c < kCols / 16; ++c) {  // sixteen at a time: 128 sums leave no more registers
+              if (n0 + 16 * c >= P.N) break;
+              uint32_t v[16];
+              tmem_ld16(tb + 16 * c, v);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) sum[16 * c + i] += __uint_as_float(v[i]);
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_relaxed(&tempty[acc], 0);
+          acc_phase ^= 1u << acc;
+          acc ^= 1;
+        }
+        if (ok_all && m < end) {
+#pragma unroll
+          for (int c = 0; c < kCols / 32; ++c) {
+            const int col = n0 + 32 * c;
+            if (col >= P.N) break;
+            // the tile's last store has been read
+            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            __syncwarp();
+#pragma unroll
+            for (int x = 0; x < 32; x += 16) {
+              uint32_t v[16] = {};
+              if (segs) {
+                tmem_ld16(tb + 32 * c + x, v);
+                tmem_ld_wait();
+              }
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float* f = &sum[32 * c + x + 4 * i];
+                *piece(t, lane, x / 4 + i) = make_uint4(
+                    __float_as_uint(f[0] + __uint_as_float(v[4 * i])), __float_as_uint(f[1] + __uint_as_float(v[4 * i + 1])),
+                    __float_as_uint(f[2] + __uint_as_float(v[4 * i + 2])), __float_as_uint(f[3] + __uint_as_float(v[4 * i + 3])));
+              }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              if (P.accumulate) add_3d(&TM.o, t, col, m, it.e);
+              else store_3d(&TM.o, t, col, m, it.e);
+              asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            }
+          }
+        }
+        if (segs && ok_all) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_relaxed(&tempty[acc], 0);
+          acc_phase ^= 1u << acc;
+          acc ^= 1;
+        }
+      }
+      for (int h = 0; !R::split && h < it.nh; ++h) {
         const int a = NH == 1 ? acc : h;
         const int n = it.n + h;
         // 16-byte pieces of a row of es-byte values that lie left of column N
@@ -650,12 +749,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<KIND, NH>::kT
             }
           }
         } else if (LY::staged && some) {
-          // dW, often short reductions under large results, where the writes bound: whole 128-byte
-          // lines leave through the TMA, which also clips ragged edges and adds to fp32. fp32 dW of 64
-          // experts of 4096 x 2048: over 8 rows each 339 us (6.3 TB/s), 444 from registers; over 512 rows
-          // 566 and 582; from 1024 on the two meet. A second buffer a warp, for a stage of the ring less,
-          // or sixteen warps of one: 355 -> 359 and 361 us over 8 rows, 557 -> 615 and 637 over 512.
-          constexpr int W = KIND == kKWeight32 ? 32 : 64;
+          // bf16 dW of short reductions: whole 128-byte lines through the TMA, as fp32 ones
+          constexpr int W = 64;
           uint8_t* const t = smem + LY::out + (size_t)(warp - 2) * OUT_BYTES;
           const int n0 = n * 256;
 #pragma unroll 1
@@ -676,31 +771,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<KIND, NH>::kT
 #pragma unroll
                 for (int i = 0; i < 32; ++i) v[i] = 0;
               }
-              if (KIND == kKWeight32) {
+              if (P.accumulate && store) add_old(v, out + (int64_t)(col + x) * 2, wide, left(col + x, 2));
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                  *piece(t, lane, i) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-              } else {
-                if (P.accumulate && store) add_old(v, out + (int64_t)(col + x) * 2, wide, left(col + x, 2));
+              for (int i = 0; i < 4; ++i) {
+                uint32_t p4[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  uint32_t p4[4];
-#pragma unroll
-                  for (int j = 0; j < 4; ++j)
-                    p4[j] = pack_bf16(__uint_as_float(v[8 * i + 2 * j]), __uint_as_float(v[8 * i + 2 * j + 1]));
-                  *piece(t, lane, x / 8 + i) = make_uint4(p4[0], p4[1], p4[2], p4[3]);
-                }
+                for (int j = 0; j < 4; ++j)
+                  p4[j] = pack_bf16(__uint_as_float(v[8 * i + 2 * j]), __uint_as_float(v[8 * i + 2 * j + 1]));
+                *piece(t, lane, x / 8 + i) = make_uint4(p4[0], p4[1], p4[2], p4[3]);
               }
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-              if (KIND == kKWeight32 && P.accumulate) add_3d(&TM.o, t, col, m, it.e);
-              else store_3d(&TM.o, t, col, m, it.e);
+              store_3d(&TM.o, t, col, m, it.e);
               asm volatile("cp.async.bulk.commit_group;" ::: "memory");
             }
           }
-        } else if (some) {  // down, up_grad, dW
+        } else if (some) {  // down, up_grad, bf16 dW of long reductions
           const int n0 = n * 256;
 #pragma unroll 1
           for (int c = part * kCols; c < (part + 1) * kCols; c += 32) {
@@ -716,22 +804,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<KIND, NH>::kT
 #pragma unroll
               for (int i = 0; i < 32; ++i) v[i] = 0;
             }
-            if (!store) {
-            } else if (KIND == kKWeight32) {
-              const int k = left(col, 4);
-              if (P.accumulate) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  uint32_t o[8];
-                  get32(out + (int64_t)col * 4 + 32 * i, o, wide, k - 2 * i);
-#pragma unroll
-                  for (int j = 0; j < 8; ++j)
-                    v[8 * i + j] = __float_as_uint(__uint_as_float(v[8 * i + j]) + __uint_as_float(o[j]));
-                }
-              }
-              put64(out + (int64_t)col * 4, v, wide, k);
-              put64(out + (int64_t)col * 4 + 64, v + 16, wide, k - 4);
-            } else {
+            if (store) {
               const int k = left(col, 2);
               if (R::weight && P.accumulate) add_old(v, out + (int64_t)col * 2, wide, k);
               uint32_t pr[16];
@@ -815,14 +888,13 @@ static moe_status_t launch(const Maps& tm, Params P, int64_t max_rows_items, int
 // 8 to 64 experts of 512 to 4096 rows, narrow against wide, us: up 2048 long 419 and 460, 4096 1326
 // and 1290, 8192 1530 and 1392; down 1024 197 and 211, 2048 757 and 720, 14336 687 and 648; up_grad 2048
 // 380 and 361, 4096 390 and 348; bf16 weights over 512 rows 247 and 271, 1024 1381 and 1396, 2048
-// 1510 and 1412; fp32 ones over 2048 rows 393 and 414, 4096 382 and 370. Down_grad, whose epilogue reads
-// the most, lost at every length (8192: 889 against 874 at best, 4096 801 and 935): it has no wide form.
+// 1510 and 1412. Down_grad, whose epilogue reads the most, lost at every length (8192: 889 against 874 at best,
+// 4096 801 and 935): it has no wide form, nor have fp32 weights, whose sums fill the registers.
 template <int KIND>
 constexpr int kWideFrom = KIND == kKUp         ? 4096
                           : KIND == kKDown     ? 2048
                           : KIND == kKUpGrad   ? 2048
                           : KIND == kKWeight16 ? 1536
-                          : KIND == kKWeight32 ? 2560
                                                : 0;
 // And from this many wide items a resident CTA pair on: with fewer, the last round leaves too many
 // pairs without work.

@@ -95,6 +95,23 @@ __device__ __forceinline__ bool wait_bounded(uint64_t* b, uint32_t parity,
   if (mbar_try_wait(b, parity)) return true;
   return wait_slow(b, parity, abort_flag, status);
 }
+// The same without a call, for code that holds more registers than a call leaves alone.
+__device__ __forceinline__ bool wait_bounded_inline(uint64_t* b, uint32_t parity,
+                                                    volatile int* abort_flag, int* status) {
+  const uint64_t t0 = gtimer();
+#pragma unroll 1
+  for (uint32_t it = 1; !mbar_try_wait(b, parity); ++it) {
+    if ((it & 63u) == 0) {
+      if (*abort_flag) return false;
+      if (gtimer() - t0 > kTimeoutNs) {
+        *abort_flag = 1;
+        atomicExch(status, kStatusTimeout);
+        return false;
+      }
+    }
+  }
+  return true;
+}
 constexpr uint32_t kSleepNs = 1000;  // suspend hint of the sleeping waits
 __device__ __forceinline__ bool wait_bounded_sleep(uint64_t* b, uint32_t parity,
                                                    volatile int* abort_flag, int* status) {

@@ -127,3 +127,27 @@ def test_permute_of_copies_past_l2(M, L, k):
     want[sid[live].long()] = torch.arange(len(sid), dtype=torch.int32, device=DEV)[live]
     assert torch.equal(pos.view(-1), want)
     assert L.moe_device_status(True) == 1  # the dropped slots
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_fp32_weight_gradients_of_long_runs_keep_their_precision(M, accumulate):
+    """The tensor cores' accumulators cut off: half a unit a step on average, always toward zero. 512 rows are
+    32 steps of 16, so 32 half units of 2^-23 of the sum where the sums leave the accumulators by then, however
+    long the run; over 8192 rows in one go it would be 16 times that."""
+    counts = [512, 513, 0, 1023, 1024, 1040, 100, 8192, 4097]
+    rs, P = runs(counts)
+    g = gen(7)
+    live = torch.zeros(P, 1, dtype=torch.bool, device=DEV)
+    for _, r in rs:
+        live[r] = True
+    dy, a = randn(g, P, 264, dtype=BF) * live, randn(g, P, 520, dtype=BF) * live
+    cnt = torch.tensor(counts, dtype=torch.int32, device=DEV)
+    dW = randn(g, len(counts), 264, 520)
+    before = dW.to(F64)
+    if accumulate:
+        M.expert_weight_grad(dy, a, cnt, out=dW, accumulate=True)
+    else:
+        dW, before = M.expert_weight_grad(dy, a, cnt, out_dtype=F32), torch.zeros_like(before)
+    for e, r in rs:
+        want = before[e] + dy[r].to(F64).T @ a[r].to(F64)
+        assert (dW[e].to(F64) - want).norm() <= 32 * 2.0 ** -24 * want.norm(), counts[e]
