@@ -107,7 +107,8 @@ moe_status_t moe_expert_up_backward(const moe_experts_t* cfg, const void* dh13, 
  * N = H). dtype is that of dy and a; out_dtype (MOE_F32, or MOE_BF16 when dtype is) that of
  * dW. accumulate 0: dW is overwritten (zeros for an expert without rows); 1: added to, the sum
  * rounded once. The tensor cores' accumulators cut off rather than round; fp32 dW of bf16 rows leaves them
- * every 512 rows and is added up in rounded fp32 (off by 4.8e-7 of its size over 512 to 8192 rows). */
+ * every 512 rows and is added up in rounded fp32 (off by 4.8e-7 of its size over 512 to 8192 rows). fp32
+ * products and their gradients sum in fp32, reductions of more than 2048 steps in spans of 512. */
 moe_status_t moe_expert_weight_grad(int rows, int E, int M, int N, moe_dtype_t dtype,
                                     moe_dtype_t out_dtype, int accumulate, const void* dy,
                                     const void* a, const int32_t* counts, void* dW,

@@ -151,3 +151,52 @@ def test_fp32_weight_gradients_of_long_runs_keep_their_precision(M, accumulate):
     for e, r in rs:
         want = before[e] + dy[r].to(F64).T @ a[r].to(F64)
         assert (dW[e].to(F64) - want).norm() <= 32 * 2.0 ** -24 * want.norm(), counts[e]
+
+
+def off(got, want, what):
+    """Sums of fp32 products, rounded as they go: a random walk of half units. Spans of 512 steps whose totals
+    are added up stay below sqrt(512) of them, however long the reduction."""
+    assert (got.to(F64) - want).norm() <= 512 ** 0.5 * U * want.norm(), what
+
+
+@pytest.mark.parametrize("counts", [[2, 0, 31], [700, 5, 1500]])  # tiles of 32 rows, of 128
+def test_fp32_products_of_long_reductions_keep_their_precision(M, counts):
+    rs, P = runs(counts)
+    g, long, short = gen(len(counts)), 15600, 72
+    E, cnt = len(counts), torch.tensor(counts, dtype=torch.int32, device=DEV)
+    live = torch.zeros(P, 1, dtype=torch.bool, device=DEV)
+    for _, r in rs:
+        live[r] = True
+    # down: sums over I; the gradient of up: over 2 I; up and the gradient of down: over H
+    act, dh13 = randn(g, P, long) * live, randn(g, P, long) * live
+    xs, dys = randn(g, P, long) * live, randn(g, P, long) * live
+    W2, W13 = randn(g, E, short, long), randn(g, E, long, short)
+    U13, D2 = randn(g, E, 2 * short, long, std=long ** -0.5), randn(g, E, long, short, std=long ** -0.5)
+    h13 = torch.ones(P, 2 * short, device=DEV)  # dup = dact silu(1)
+    ys, dxs = M.expert_down(act, W2, cnt), M.expert_up_backward(dh13, W13, cnt)
+    up, (dd, _) = M.expert_up(xs, U13, cnt)[0], M.expert_down_backward(dys, D2, h13, cnt)
+    silu = torch.sigmoid(torch.ones((), dtype=F64, device=DEV))
+    for e, r in rs:
+        if r.start == r.stop:
+            continue
+        d = lambda t: t.to(F64)  # noqa: E731
+        off(ys[r], d(act[r]) @ d(W2[e]).T, "ys")
+        off(dxs[r], d(dh13[r]) @ d(W13[e]), "dxs")
+        off(up[r], d(xs[r]) @ d(U13[e]).T, "h13")
+        off(dd[r][:, short:], silu * (d(dys[r]) @ d(D2[e])), "dup")
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_fp32_weight_gradients_of_fp32_rows_keep_their_precision(M, accumulate):
+    counts = [511, 512, 513, 0, 1024, 8192, 15601]
+    rs, P = runs(counts)
+    g = gen(8)
+    live = torch.zeros(P, 1, dtype=torch.bool, device=DEV)
+    for _, r in rs:
+        live[r] = True
+    dy, a = randn(g, P, 136) * live, randn(g, P, 264) * live
+    dW = randn(g, len(counts), 136, 264) if accumulate else torch.zeros(len(counts), 136, 264, device=DEV)
+    before = dW.to(F64)
+    M.expert_weight_grad(dy, a, torch.tensor(counts, dtype=torch.int32, device=DEV), out=dW, accumulate=accumulate)
+    for e, r in rs:
+        off(dW[e], before[e] + dy[r].to(F64).T @ a[r].to(F64), counts[e])
