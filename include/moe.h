@@ -362,8 +362,8 @@ moe_status_t moe_selftest_wait_timeout(cudaStream_t stream);
 /* Diagnostic (synchronises the current device): returns the device status word (0 = no
  * fault seen; 1 = an expert id outside [0, E); 2 = a wait ran out of time; 3 = the
  * two CTAs of a tensor-core pair were given different tensor-memory columns; 4 = expert
- * counts that do not fit in a training row buffer, moe_train.h) and clears it when
- * reset != 0. Not for use inside stream capture. */
+ * counts that do not fit in a training row buffer, moe_train.h; 5 = sequence offsets that
+ * decrease or lie outside the tokens, moe_stack.h) and clears it when reset != 0. Not for use inside stream capture. */
 int moe_device_status(int reset);
 
 #ifdef __cplusplus

@@ -3,7 +3,8 @@
 The layer runs in ``libmoe_gb300.so`` (hand-written CUDA for sm_103a behind the C ABI of
 ``include/moe.h``). This package is the Python binding (``_lib``, same function names as
 the C ABI), ``layer.MoELayer``, which owns the workspace and calls ``moe_forward``, and
-``training``, the operators of a training step (``include/moe_train.h``) on tensors.
+``training``, the operators of a training step (``include/moe_train.h`` and ``moe_stack.h``) on
+tensors.
 """
 from ._lib import (EXPORTED, MOE_BF16, MOE_F32, MOE_GEMM_DECODE_TC,  # noqa: F401
                    MOE_GEMM_INVALID, MOE_GEMM_PAIR_TC, MOE_GEMM_SIMT, MOE_GEMM_SMALL_BATCH,
@@ -27,3 +28,8 @@ from ._lib import (MOE_GATE_CHANNEL, MOE_GATE_FULL, MOE_GATE_NONE, MOE_GATE_TOKE
                    moe_expert_up_backward, moe_expert_weight_grad, moe_experts_t, moe_permute,
                    moe_permute_backward, moe_route_backward, moe_unpermute,
                    moe_unpermute_backward)
+from ._lib import (moe_balance_loss, moe_balance_loss_backward, moe_balance_t,  # noqa: F401
+                   moe_balance_workspace_size, moe_drop_t, moe_dropout, moe_dropout_join,
+                   moe_dropout_join_backward, moe_embed, moe_embed_backward,
+                   moe_embed_workspace_size, moe_layer_norm, moe_layer_norm_backward, moe_layer_t,
+                   moe_layer_workspace_size)

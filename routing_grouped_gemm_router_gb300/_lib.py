@@ -1,5 +1,5 @@
-"""ctypes binding of libmoe_gb300.so: the C ABI of include/moe.h and moe_train.h under the same
-names.
+"""ctypes binding of libmoe_gb300.so: the C ABI of include/moe.h, moe_train.h and moe_stack.h
+under the same names.
 
 Argument marshalling only: tensors become device pointers (``data_ptr()``), streams become
 ``cudaStream_t`` handles, and a non-OK status raises ``MoeError``. Every step of the layer
@@ -58,6 +58,21 @@ class moe_block_t(ctypes.Structure):
                 ("offset", ctypes.c_float), ("eps", ctypes.c_float)]
 
 
+class moe_layer_t(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int), ("H", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("eps", ctypes.c_float), ("scale", ctypes.c_float)]
+
+
+class moe_drop_t(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_double), ("rng", ctypes.c_void_p), ("site", ctypes.c_uint32)]
+
+
+class moe_balance_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("T", "E", "k", "n_shared", "mode")] + \
+               [("logit_bias", ctypes.c_void_p), ("S", ctypes.c_int),
+                ("offsets", ctypes.c_void_p), ("mask", ctypes.c_void_p)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing: build it with "
@@ -66,6 +81,8 @@ def _load():
     P, I32, SZ, ST = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_int
     CFG = ctypes.POINTER(moe_config_t)
     EXP, BLK = ctypes.POINTER(moe_experts_t), ctypes.POINTER(moe_block_t)
+    LAY, DRP, BAL = (ctypes.POINTER(t) for t in (moe_layer_t, moe_drop_t, moe_balance_t))
+    F32 = ctypes.c_float
     sig = {
         "moe_abi_version": (I32, []),
         "moe_status_string": (ctypes.c_char_p, [ST]),
@@ -114,6 +131,18 @@ def _load():
         "moe_block_join": (ST, [BLK, P, P, P, P, P, P, P, P, P, P]),
         "moe_block_join_backward": (ST, [BLK] + [P] * 15 + [SZ, P]),
         "moe_route_backward": (ST, [CFG, P, P, P, P, P]),
+        "moe_embed": (ST, [P, I32, I32, P, I32, I32, I32, F32, P, P]),
+        "moe_embed_workspace_size": (ST, [I32, I32, I32, ctypes.POINTER(SZ)]),
+        "moe_embed_backward": (ST, [P, P, I32, I32, I32, I32, I32, I32, F32, I32, P, P, SZ, P]),
+        "moe_dropout": (ST, [LAY, DRP, P, P, P]),
+        "moe_layer_workspace_size": (ST, [LAY, ctypes.POINTER(SZ)]),
+        "moe_layer_norm": (ST, [LAY, P, P, P, P, P, P, P]),
+        "moe_layer_norm_backward": (ST, [LAY] + [P] * 10 + [SZ, P]),
+        "moe_dropout_join": (ST, [LAY, DRP] + [P] * 9),
+        "moe_dropout_join_backward": (ST, [LAY, DRP] + [P] * 11 + [SZ, P]),
+        "moe_balance_workspace_size": (ST, [BAL, ctypes.POINTER(SZ)]),
+        "moe_balance_loss": (ST, [BAL] + [P] * 8 + [SZ, P]),
+        "moe_balance_loss_backward": (ST, [BAL] + [P] * 5 + [I32, P, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -138,7 +167,11 @@ EXPORTED = ("moe_abi_version", "moe_status_string", "moe_block_m", "moe_small_ba
             "moe_expert_up", "moe_expert_down", "moe_expert_down_backward",
             "moe_expert_up_backward", "moe_expert_weight_grad", "moe_block_workspace_size",
             "moe_block_norm", "moe_block_norm_backward", "moe_block_join",
-            "moe_block_join_backward", "moe_route_backward")
+            "moe_block_join_backward", "moe_route_backward",
+            "moe_embed", "moe_embed_workspace_size", "moe_embed_backward", "moe_dropout",
+            "moe_layer_workspace_size", "moe_layer_norm", "moe_layer_norm_backward",
+            "moe_dropout_join", "moe_dropout_join_backward", "moe_balance_workspace_size",
+            "moe_balance_loss", "moe_balance_loss_backward")
 
 
 def lib():
@@ -468,3 +501,81 @@ def moe_route_backward(cfg, logits, topk_ids, dtopk_w, dlogits, stream=None):
     _check("moe_route_backward", _lib.moe_route_backward(
         ctypes.byref(cfg), _ptr(logits), _ptr(topk_ids), _ptr(dtopk_w), _ptr(dlogits),
         _stream(stream)))
+
+
+# ------------------------------------------------------------- operators around a stack's blocks
+
+def _size(name, *a) -> int:
+    out = ctypes.c_size_t(0)
+    _check(name, getattr(_lib, name)(*a, ctypes.byref(out)))
+    return out.value
+
+
+def moe_embed(tokens, token_bytes, T, table, V, H, dtype, scale, out, stream=None):
+    _check("moe_embed", _lib.moe_embed(_ptr(tokens), token_bytes, T, _ptr(table), V, H, dtype,
+                                       scale, _ptr(out), _stream(stream)))
+
+
+def moe_embed_workspace_size(T, V, H) -> int:
+    return _size("moe_embed_workspace_size", T, V, H)
+
+
+def moe_embed_backward(dx, tokens, token_bytes, T, V, H, dtype, out_dtype, scale, accumulate, dtable,
+                       ws, ws_bytes, stream=None):
+    _check("moe_embed_backward", _lib.moe_embed_backward(
+        _ptr(dx), _ptr(tokens), token_bytes, T, V, H, dtype, out_dtype, scale,
+        int(bool(accumulate)), _ptr(dtable), _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def moe_dropout(cfg, drop, x, out, stream=None):
+    _check("moe_dropout", _lib.moe_dropout(ctypes.byref(cfg), ctypes.byref(drop), _ptr(x),
+                                           _ptr(out), _stream(stream)))
+
+
+def moe_layer_workspace_size(cfg) -> int:
+    return _size("moe_layer_workspace_size", ctypes.byref(cfg))
+
+
+def moe_layer_norm(cfg, x, gamma, beta, h, mean, rstd, stream=None):
+    _check("moe_layer_norm", _lib.moe_layer_norm(
+        ctypes.byref(cfg), _ptr(x), _ptr(gamma), _ptr(beta), _ptr(h), _ptr(mean), _ptr(rstd),
+        _stream(stream)))
+
+
+def moe_layer_norm_backward(cfg, dh, x, gamma, mean, rstd, dres, dx, dgamma, dbeta, ws, ws_bytes,
+                            stream=None):
+    _check("moe_layer_norm_backward", _lib.moe_layer_norm_backward(
+        ctypes.byref(cfg), _ptr(dh), _ptr(x), _ptr(gamma), _ptr(mean), _ptr(rstd), _ptr(dres),
+        _ptr(dx), _ptr(dgamma), _ptr(dbeta), _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def moe_dropout_join(cfg, drop, x, y, gamma_next, beta_next, out, h, mean, rstd, stream=None):
+    _check("moe_dropout_join", _lib.moe_dropout_join(
+        ctypes.byref(cfg), ctypes.byref(drop), _ptr(x), _ptr(y), _ptr(gamma_next),
+        _ptr(beta_next), _ptr(out), _ptr(h), _ptr(mean), _ptr(rstd), _stream(stream)))
+
+
+def moe_dropout_join_backward(cfg, drop, dres, dh, out, gamma_next, mean, rstd, dx, dy, dgamma_next,
+                              dbeta_next, ws, ws_bytes, stream=None):
+    _check("moe_dropout_join_backward", _lib.moe_dropout_join_backward(
+        ctypes.byref(cfg), ctypes.byref(drop), _ptr(dres), _ptr(dh), _ptr(out),
+        _ptr(gamma_next), _ptr(mean), _ptr(rstd), _ptr(dx), _ptr(dy), _ptr(dgamma_next),
+        _ptr(dbeta_next), _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def moe_balance_workspace_size(cfg) -> int:
+    return _size("moe_balance_workspace_size", ctypes.byref(cfg))
+
+
+def moe_balance_loss(cfg, logits, topk_ids, losses, counts, tokens, prob, totals, ws, ws_bytes,
+                     stream=None):
+    _check("moe_balance_loss", _lib.moe_balance_loss(
+        ctypes.byref(cfg), _ptr(logits), _ptr(topk_ids), _ptr(losses), _ptr(counts), _ptr(tokens),
+        _ptr(prob), _ptr(totals), _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def moe_balance_loss_backward(cfg, dlosses, logits, counts, tokens, totals, accumulate, dlogits,
+                              stream=None):
+    _check("moe_balance_loss_backward", _lib.moe_balance_loss_backward(
+        ctypes.byref(cfg), _ptr(dlosses), _ptr(logits), _ptr(counts), _ptr(tokens), _ptr(totals),
+        int(bool(accumulate)), _ptr(dlogits), _stream(stream)))

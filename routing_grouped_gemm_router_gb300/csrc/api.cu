@@ -4,6 +4,7 @@
 #include <mutex>
 
 #include "common.cuh"
+#include "stack.cuh"
 #include "train.cuh"
 
 namespace moe {
@@ -655,7 +656,8 @@ int moe_device_status(int reset) {
   const int t = tiny_status_read(reset);
   const int d = dec_status_read(reset);
   const int e = train_status_read(reset);
-  return g ? g : (d ? d : (r ? r : (a ? a : (t ? t : (c ? c : e)))));
+  const int b = balance_status_read(reset);
+  return g ? g : (d ? d : (r ? r : (a ? a : (t ? t : (c ? c : (e ? e : b))))));
 }
 
 }  // extern "C"

@@ -279,37 +279,13 @@ __global__ void __launch_bounds__(kThreadsOf<VPT>)
     }
   }
 
-  // The CTA's column sums: its groups' sums are added in order through shared memory (the ring,
-  // whose copies have all landed), then leave as a partial row, or as the result of a lone CTA.
-  auto leave = [&](F2 (&s)[VPT][4], int kind, float factor) {
-    float* to = gridDim.x == 1 ? outs.p[kind]
-                               : A.ws + ((int64_t)blockIdx.x * kinds + kind) * S.H;
-    float* all = S.per > 1 ? (float*)smem + (int64_t)local * S.H : to;
-    if (S.per > 1) __syncthreads();
-#pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-      const int c = g + v * S.group;
-      if (c >= S.chunks) continue;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float lo, hi;
-        split(s[v][i], lo, hi);
-        all[c * 8 + 2 * i] = lo * factor;
-        all[c * 8 + 2 * i + 1] = hi * factor;
-      }
-    }
-    if (S.per == 1) return;
-    __syncthreads();
-    for (int c = threadIdx.x; c < S.H; c += blockDim.x) {
-      float sum = 0.f;
-      for (int l = 0; l < S.per; ++l) sum += ((const float*)smem)[l * S.H + c];
-      to[c] = sum;
-    }
-  };
   int kind = 0;
-  if constexpr (JOIN) leave(sp, kind++, EACH ? S.scale : 1.f);
-  if (next) leave(sn, kind++, 1.f);
-  if constexpr (CHANNEL) leave(sg, kind++, S.scale);
+  auto leave = [&](const F2 (&s)[VPT][4], float factor) {
+    leave_columns<VPT>(S, smem, local, g, s, kind++, kinds, factor, A.ws, outs);
+  };
+  if constexpr (JOIN) leave(sp, EACH ? S.scale : 1.f);
+  if (next) leave(sn, 1.f);
+  if constexpr (CHANNEL) leave(sg, S.scale);
 }
 
 // Chunks of 8 elements a thread holds. More of them share the fixed cost of a warp's row (the

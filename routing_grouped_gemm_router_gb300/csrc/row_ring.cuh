@@ -217,6 +217,37 @@ struct Outs {
   float* p[3];
 };
 
+// A thread's column sums after its last row: the CTA's groups' sums are added in order through shared
+// memory (the ring, whose copies have all landed), then leave as a partial row, or as the result of a
+// lone CTA. Called by all threads.
+template <int VPT>
+__device__ __forceinline__ void leave_columns(const Shape& S, uint8_t* smem, int local, int g,
+                                              const F2 (&s)[VPT][4], int kind, int kinds,
+                                              float factor, float* ws, const Outs& outs) {
+  float* to = gridDim.x == 1 ? outs.p[kind] : ws + ((int64_t)blockIdx.x * kinds + kind) * S.H;
+  float* all = S.per > 1 ? (float*)smem + (int64_t)local * S.H : to;
+  if (S.per > 1) __syncthreads();
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    const int c = g + v * S.group;
+    if (c >= S.chunks) continue;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float lo, hi;
+      split(s[v][i], lo, hi);
+      all[c * 8 + 2 * i] = lo * factor;
+      all[c * 8 + 2 * i + 1] = hi * factor;
+    }
+  }
+  if (S.per == 1) return;
+  __syncthreads();
+  for (int c = threadIdx.x; c < S.H; c += blockDim.x) {
+    float sum = 0.f;
+    for (int l = 0; l < S.per; ++l) sum += ((const float*)smem)[l * S.H + c];
+    to[c] = sum;
+  }
+}
+
 // Column sums of the partial rows: part[rows][kinds][H] -> out[kind][H]. A block takes 32
 // columns; each of its 32 warps adds every 32nd row, then their sums are added in order.
 static __global__ void __launch_bounds__(1024) column_sum_kernel(const float* __restrict__ part, int rows,
