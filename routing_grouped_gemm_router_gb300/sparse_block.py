@@ -1,8 +1,9 @@
-"""A trainable stack of sparse blocks on the operators of ``training``:
+"""Trainable stacks of sparse blocks on the operators of ``training``. SparseStack:
 
     x <- x + scale * gate . norm(MoE(norm(x)))        for every block,
 
 a norm before and after the MoE layer (RMS, fp32 weights), an optional gate, a residual scale.
+TokenStack (token_stack.py) trains blocks x <- x + scale * dropout(MoE(layer_norm(x))) from token ids.
 Forward and backward are explicit calls: ``forward`` keeps what the backward pass needs,
 ``backward`` takes the gradient of the output and adds to gradients that the stack owns, so a
 whole step allocates from PyTorch's pool only and can be captured in a CUDA graph.
@@ -36,17 +37,14 @@ def _fits(name, t, shape, dtype, device):
         raise ValueError(f"{name}: is on {t.device}, expected {device}")
 
 
-class SparseBlock:
-    """Parameters of one block. Wg[E, H], W13[E', 2I, H], W2[E', H, I] all in bf16 or all in fp32 (E' =
-    E + n_shared: shared experts follow the routed ones), gamma_in[H] and gamma_out[H] fp32; gate: None
-    or fp32 [H], the same for all tokens (where the number of tokens is fixed, any gate of block_join);
-    logit_bias, select_bias: None or fp32 [E]. All contiguous, on one device; anything else raises
-    ValueError."""
+class SparseLayer:
+    """Router and experts of one block: Wg[E, H], W13[E', 2I, H], W2[E', H, I] all in bf16 or all in fp32
+    (E' = E + n_shared: shared experts follow the routed ones); logit_bias, select_bias: None or fp32
+    [E]. All contiguous, on one device; anything else raises ValueError."""
 
-    def __init__(self, Wg, W13, W2, gamma_in, gamma_out, k: int, gate=None, scale: float = 1.0,
-                 mode: int = L.MOE_ROUTE_SOFTMAX, renormalize: bool = True,
+    def __init__(self, Wg, W13, W2, k: int, mode: int = L.MOE_ROUTE_SOFTMAX, renormalize: bool = True,
                  router_scale: float = 1.0, n_group: int = 1, topk_group: int = 1,
-                 logit_bias=None, select_bias=None, n_shared: int = 0, eps: float = 1e-6):
+                 logit_bias=None, select_bias=None, n_shared: int = 0):
         if not isinstance(Wg, torch.Tensor) or Wg.dim() != 2 or Wg.dtype not in (torch.bfloat16, torch.float32):
             raise ValueError("Wg: a bfloat16 or float32 tensor [E, H] is needed")
         for name, t in (("W13", W13), ("W2", W2)):
@@ -58,21 +56,14 @@ class SparseBlock:
             raise ValueError(f"W13 {tuple(W13.shape)}, W2 {tuple(W2.shape)}, Wg {tuple(Wg.shape)}: "
                              "extents do not belong together")
         self.Wg, self.W13, self.W2 = Wg, W13, W2
-        self.gamma_in, self.gamma_out, self.gate = gamma_in, gamma_out, gate
         self.E, self.H = Wg.shape
         self.I, self.k, self.n_shared = W2.shape[2], k, n_shared
-        self.scale, self.eps = scale, eps
         self.mode, self.renormalize, self.router_scale = mode, renormalize, router_scale
         self.n_group, self.topk_group = n_group, topk_group
         self.logit_bias, self.select_bias = logit_bias, select_bias
         self._check_router()
-        for name, t in (("gamma_in", gamma_in), ("gamma_out", gamma_out)):
-            _fits(name, t, (self.H,), torch.float32, Wg.device)
-        if gate is not None:
-            rank = gate.dim() if isinstance(gate, torch.Tensor) else 1
-            full = rank == 2 and gate.shape[1] != 1
-            _fits("gate", gate, (self.H,) if rank == 1 else (None, self.H if full else 1),
-                  Wg.dtype if full else torch.float32, Wg.device)
+
+    names = ("Wg", "W13", "W2")  # of the tensors that train
 
     def _check_router(self):
         """What moe_route is given by address besides the tokens."""
@@ -89,7 +80,7 @@ class SparseBlock:
 
     def parameters(self):
         """name -> tensor, of those that train."""
-        p = {n: getattr(self, n) for n in ("Wg", "W13", "W2", "gamma_in", "gamma_out", "gate")}
+        p = {n: getattr(self, n) for n in self.names}
         return {n: t for n, t in p.items() if t is not None}
 
     def route(self, h):
@@ -116,8 +107,9 @@ class SparseBlock:
         return ops.unpermute(ys, pos, w), MoESaved(h, logits, ids, w, table.sorted_ids, table.counts, pos,
                                                    xs, h13, ys)
 
-    def moe_backward(self, dy, s: "MoESaved", grads: dict):
-        """dh; gradients of Wg, W13 and W2 are added to grads (fp32 tensors of their shapes)."""
+    def moe_backward(self, dy, s: "MoESaved", grads: dict, balance: Optional["BalanceGrads"] = None):
+        """dh; gradients of Wg, W13 and W2 are added to grads (fp32 tensors of their shapes). balance: the
+        router's losses that go into the total, if any."""
         dys, dw = ops.unpermute_backward(dy, s.ys, s.sorted_ids, s.row_pos, s.topk_w)
         dh13, act = ops.expert_down_backward(dys, self.W2, s.h13, s.counts)
         ops.expert_weight_grad(dys, act, s.counts, out=grads["W2"], accumulate=True)
@@ -125,10 +117,46 @@ class SparseBlock:
         dh = ops.permute_backward(ops.expert_up_backward(dh13, self.W13, s.counts), s.row_pos)
         dlogits = ops.route_backward(s.logits, s.topk_ids, dw, self.mode, self.renormalize,
                                      self.router_scale, self.logit_bias, self.n_shared)
+        if balance is not None:
+            ops.balance_loss_backward(balance.dlosses, s.logits, balance.saved, self.k, self.mode, self.logit_bias,
+                                      balance.offsets, balance.mask, dlogits=dlogits)
         grads["Wg"].addmm_(dlogits.T, s.h.float())
         # with bf16 weights dlogits is rounded to bf16 here, as the product of two bf16 matrices takes it:
         # each term is then off by at most 2^-8 of itself, as h and Wg are, and the sum over experts is fp32
         return torch.addmm(dh, dlogits.to(dh.dtype), self.Wg)
+
+
+class SparseBlock(SparseLayer):
+    """A SparseLayer and the norms around it: gamma_in[H] and gamma_out[H] fp32; gate: None or fp32 [H], the
+    same for all tokens (where the number of tokens is fixed, any gate of block_join). All contiguous, on
+    one device; anything else raises ValueError."""
+
+    names = ("Wg", "W13", "W2", "gamma_in", "gamma_out", "gate")
+
+    def __init__(self, Wg, W13, W2, gamma_in, gamma_out, k: int, gate=None, scale: float = 1.0,
+                 mode: int = L.MOE_ROUTE_SOFTMAX, renormalize: bool = True,
+                 router_scale: float = 1.0, n_group: int = 1, topk_group: int = 1,
+                 logit_bias=None, select_bias=None, n_shared: int = 0, eps: float = 1e-6):
+        super().__init__(Wg, W13, W2, k, mode, renormalize, router_scale, n_group, topk_group, logit_bias,
+                         select_bias, n_shared)
+        self.gamma_in, self.gamma_out, self.gate = gamma_in, gamma_out, gate
+        self.scale, self.eps = scale, eps
+        for name, t in (("gamma_in", gamma_in), ("gamma_out", gamma_out)):
+            _fits(name, t, (self.H,), torch.float32, Wg.device)
+        if gate is not None:
+            rank = gate.dim() if isinstance(gate, torch.Tensor) else 1
+            full = rank == 2 and gate.shape[1] != 1
+            _fits("gate", gate, (self.H,) if rank == 1 else (None, self.H if full else 1),
+                  Wg.dtype if full else torch.float32, Wg.device)
+
+
+class BalanceGrads(NamedTuple):
+    """The router's losses in a total: their weights (fp32 [2] on the device), what ``balance_loss`` returned and
+    the sequences and tokens that it was given."""
+    dlosses: torch.Tensor
+    saved: ops.BalanceLoss
+    offsets: Optional[torch.Tensor] = None
+    mask: Optional[torch.Tensor] = None
 
 
 class MoESaved(NamedTuple):
