@@ -118,8 +118,8 @@ moe_status_t moe_dropout_join_backward(const moe_layer_t* cfg, const moe_drop_t*
  *
  * both 0 where no token takes part. The gradient runs through P, not through the counts.
  * Sequence s is tokens offsets[s] <= t < offsets[s + 1]; tokens before the first or from the last
- * offset on, and tokens whose mask byte is 0, take no part: they are not read and their dlogits
- * are 0 (or, added to, left). Offsets do not decrease and lie in [0, T]; where they do not,
+ * offset on, and tokens whose mask byte is 0, take no part, whatever their logits: their
+ * dlogits are 0 (or, added to, left). Offsets do not decrease and lie in [0, T]; where they do not,
  * device status 5 is recorded (moe_device_status) and what the call writes is unspecified. Ids outside [0, E) and the n_shared
  * slots at the end are not counted. E at most 512, k + n_shared at most 32, T at most 2^28, S at most 2^20. */
 typedef struct moe_balance {

@@ -6,11 +6,12 @@
 //   gradient, with g_e = E c_se / (k n_s) / (n_s S'):
 //     dz_e = d0 p_e (g_e - sum g p) [1 - sigma(z_e), sigmoid routing] + d1 2 l / N softmax(z)_e
 // The logits are read once each way, so HBM would bound both directions, but a batch's logits are a few
-// megabytes: launches and the latency of one token's sums count as much. A group of G lanes (a power
-// of two) takes a token, lane i holding experts i, i + G, ...; a CTA takes a chunk of consecutive tokens,
-// sequence by sequence, and leaves partial sums in slot chunk + s, a place of its own for every pair of a
-// chunk and a sequence that meet, since both only grow along the tokens. A second kernel adds a
-// sequence's slots in order. Counts are integers, everything else is added in a fixed order.
+// megabytes: instructions and latencies count as much. A group of G lanes (a power of two) takes a token,
+// up to 16 experts a lane: with a whole warp a token, the shuffles of its sums took most of the time
+// (32768 tokens of 128 experts: 16 us forward, 20 backward). A CTA takes a chunk of consecutive tokens, sequence by sequence,
+// and leaves partial sums in slot chunk + s, a place of its own for every pair of a chunk and a sequence
+// that meet, since both only grow along the tokens. A second kernel adds a sequence's slots in order.
+// Counts are integers, everything else is added in a fixed order.
 #include "stack.cuh"
 #include "train.cuh"
 
@@ -19,9 +20,9 @@ namespace balance {
 
 __device__ int g_status;
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
-constexpr int kMaxE = 512;
+constexpr int kThreads = 512, kWarps = kThreads / 32;  // forward
+constexpr int kBackThreads = 256;
+constexpr int kNear = 2048;  // offsets that are looked up in shared memory
 
 struct Args {
   const float *logits, *bias;
@@ -42,18 +43,27 @@ struct Args {
 struct Run {
   int s, end;
 };
-__device__ __forceinline__ Run run_of(const Args& A, int t, int end) {
-  if (!A.offsets) return {0, end};
-  int lo = 0, hi = A.S + 1;  // the first offset beyond t
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(A.offsets + mid) <= t) lo = mid + 1;
-    else hi = mid;
+struct Offsets {
+  int32_t near[kNear];
+  // Called by all threads of the CTA.
+  __device__ __forceinline__ void fetch(const Args& A) {
+    if (!A.offsets || A.S >= kNear) return;
+    for (int i = threadIdx.x; i <= A.S; i += blockDim.x) near[i] = __ldg(A.offsets + i);
+    __syncthreads();
   }
-  if (lo == 0) return {-1, max(t + 1, min(end, __ldg(A.offsets)))};
-  if (lo == A.S + 1) return {-1, end};
-  return {lo - 1, max(t + 1, min(end, __ldg(A.offsets + lo)))};
-}
+  __device__ __forceinline__ Run run(const Args& A, int t, int end) const {
+    if (!A.offsets) return {0, end};
+    const int32_t* off = A.S < kNear ? near : A.offsets;
+    int lo = 0, hi = A.S + 1;  // the first offset beyond t
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (off[mid] <= t) lo = mid + 1;
+      else hi = mid;
+    }
+    if (lo > A.S) return {-1, end};
+    return {lo - 1, max(t + 1, min(end, off[lo]))};
+  }
+};
 
 __device__ __forceinline__ float group_max(float v, int group) {
   for (int off = group >> 1; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
@@ -64,158 +74,169 @@ __device__ __forceinline__ float group_add(float v, int group) {
   return v;
 }
 
+// The experts of a lane: pieces of four consecutive ones, or (VEC false: E is no multiple of 4) single
+// ones, of its group in turn. Beyond the last expert e >= E.
+template <int N, bool VEC>
+__device__ __forceinline__ int expert(int i, int gl, int G) {
+  return VEC ? (i / 4 * G + gl) * 4 + i % 4 : gl + i * G;
+}
+template <int N, bool VEC>
+__device__ __forceinline__ void load_lane(const float* row, bool in, int E, int gl, int G, float beyond,
+                                          float (&v)[N]) {
+  if constexpr (VEC) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const int e = expert<N, VEC>(i, gl, G);
+      float4 q = make_float4(beyond, beyond, beyond, beyond);
+      if (in && e < E) q = __ldg((const float4*)(row + e));
+      v[i] = q.x; v[i + 1] = q.y; v[i + 2] = q.z; v[i + 3] = q.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int e = expert<N, VEC>(i, gl, G);
+      v[i] = in && e < E ? __ldg(row + e) : beyond;
+    }
+  }
+}
+
 // A token's probabilities from its logits, in the lanes of its group.
-template <int N>
+template <int N, bool SIGMOID>
 struct Token {
-  float p[N], soft[N], slope[N];  // p; softmax; 1 - sigma(z), or 1
+  float p[N];
+  float soft[SIGMOID ? N : 1], slope[SIGMOID ? N : 1];  // softmax; 1 - sigma(z)
   float lse;
   // z: -inf beyond the experts. Sigmoids are taken relative to e^max where all logits are negative: p
   // stays right where every sigmoid underflows.
-  __device__ __forceinline__ void set(const float (&z)[N], int group, bool sigmoid) {
+  __device__ __forceinline__ void set(const float (&z)[N], int group) {
     float m = -INFINITY;
 #pragma unroll
     for (int i = 0; i < N; ++i) m = fmaxf(m, z[i]);
     m = group_max(m, group);
-    float sum = 0.f;
+    float sum = 0.f, total = 0.f;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      soft[i] = expf(z[i] - m);
-      sum += soft[i];
+      p[i] = expf(z[i] - m);
+      sum += p[i];
     }
-    float total = 0.f;
-    if (sigmoid) {
+    if constexpr (SIGMOID) {
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const float x = expf(-fabsf(z[i])), d = 1.f / (1.f + x);
-        p[i] = m < 0.f ? soft[i] * d : z[i] >= 0.f ? d : x * d;
+        const float x = expf(-fabsf(z[i])), d = __fdividef(1.f, 1.f + x);
+        soft[i] = p[i];
+        p[i] = m < 0.f ? p[i] * d : z[i] >= 0.f ? d : x * d;
         slope[i] = z[i] >= 0.f ? x * d : d;
         total += p[i];
       }
+      total = group_add(total, group);
     }
     sum = group_add(sum, group);
     lse = m + logf(sum);
-    const float inv = 1.f / sum;
+    const float inv = 1.f / sum, norm = SIGMOID ? 1.f / total : inv;
 #pragma unroll
-    for (int i = 0; i < N; ++i) soft[i] *= inv;
-    if (sigmoid) {
-      const float norm = 1.f / group_add(total, group);
-#pragma unroll
-      for (int i = 0; i < N; ++i) p[i] *= norm;
-    } else {
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        p[i] = soft[i];
-        slope[i] = 1.f;
-      }
+    for (int i = 0; i < N; ++i) {
+      p[i] *= norm;
+      if constexpr (SIGMOID) soft[i] *= inv;
     }
   }
 };
 
-template <int N>
-__device__ __forceinline__ void load_logits(const Args& A, int64_t t, bool live, int gl,
-                                            float (&z)[N]) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int e = gl + i * A.group;
-    z[i] = live && e < A.E ? __ldg(A.logits + t * A.E + e) : -INFINITY;
-  }
-}
-
 // Sums over the chunks' tokens.
-template <int N>
-__global__ void __launch_bounds__(kThreads) partial_kernel(const __grid_constant__ Args A,
+template <int N, bool VEC, bool SIGMOID>
+__global__ void __launch_bounds__(kThreads, 2) partial_kernel(const __grid_constant__ Args A,
                                                            int* arrived) {
-  extern __shared__ float sums[];  // [warps][E]
-  __shared__ int cnt[kMaxE];
+  constexpr int HALF = kWarps / 2;
+  __shared__ __align__(16) float sums[HALF * 512];  // [warps / 2][E]
+  __shared__ int cnt[512];
   __shared__ float zs[kWarps];
   __shared__ int ns[kWarps];
+  __shared__ Offsets off;
   pdl_wait();
   pdl_trigger();
   if (blockIdx.x == 0 && threadIdx.x == 0) *arrived = 0;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int G = A.group, gl = lane & (G - 1), at_once = kThreads / G, sub = threadIdx.x / G;
+  const int G = A.group, gl = lane & (G - 1), groups = kThreads / G, sub = threadIdx.x / G;
   const int t0 = blockIdx.x * A.per_chunk, t1 = min(A.T, t0 + A.per_chunk);
-  float bias[N];
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int e = gl + i * G;
-    bias[i] = A.bias && e < A.E ? __ldg(A.bias + e) : 0.f;
-  }
+  off.fetch(A);
   for (int t = t0; t < t1;) {
-    const Run r = run_of(A, t, t1);
+    const Run r = off.run(A, t, t1);
     if (r.s < 0) {
       t = r.end;
       continue;
     }
     for (int e = threadIdx.x; e < A.E; e += kThreads) cnt[e] = 0;
     __syncthreads();
+    const int slots = (r.end - t) * A.slots;
+    for (int i = threadIdx.x; i < slots; i += kThreads) {
+      const int id = __ldg(A.ids + (int64_t)t * A.slots + i), j = i % A.slots;
+      const bool live = !A.mask || A.mask[t + i / A.slots];
+      if (live && j < A.k && id >= 0 && id < A.E) atomicAdd(&cnt[id], 1);
+    }
     float acc[N], z2 = 0.f;
     int n = 0;
 #pragma unroll
     for (int i = 0; i < N; ++i) acc[i] = 0.f;
-    float z[N];
-    bool live = t + sub < r.end && (!A.mask || A.mask[t + sub]);
-    load_logits<N>(A, t + sub, live, gl, z);
-    for (int b = t; b < r.end; b += at_once) {
-      const int64_t mine = (int64_t)b + sub, then = mine + at_once;
-      float zn[N];
-      const bool next = then < r.end && (!A.mask || A.mask[then]);
-      load_logits<N>(A, then, next, gl, zn);
-      if (live) {
-        for (int j = gl; j < A.k; j += G) {
-          const int id = __ldg(A.ids + mine * A.slots + j);
-          if (id >= 0 && id < A.E) atomicAdd(&cnt[id], 1);
-        }
-      }
+    for (int b = t; b < r.end; b += groups) {
+      const int64_t mine = (int64_t)b + sub;
+      const bool in = mine < r.end;
+      float z[N];
+      load_lane<N, VEC>(A.logits + mine * A.E, in, A.E, gl, G, -INFINITY, z);
+      const bool live = in && (!A.mask || A.mask[mine]);
+      if (A.bias) {
+        float bias[N];
+        load_lane<N, VEC>(A.bias, true, A.E, gl, G, 0.f, bias);
 #pragma unroll
-      for (int i = 0; i < N; ++i) z[i] += bias[i];
-      Token<N> k;
-      k.set(z, G, A.sigmoid);
+        for (int i = 0; i < N; ++i) z[i] += bias[i];
+      }
+      Token<N, SIGMOID> k;
+      k.set(z, G);
       if (live) {
 #pragma unroll
         for (int i = 0; i < N; ++i) acc[i] += k.p[i];
         z2 += k.lse * k.lse;
         ++n;
       }
-#pragma unroll
-      for (int i = 0; i < N; ++i) z[i] = zn[i];
-      live = next;
     }
-    // over a warp's tokens, then over the warps, in order
+    // over a warp's tokens, then over the warps, in a fixed order
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      for (int off = G; off < 32; off <<= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], off);
-    for (int off = G; off < 32; off <<= 1) {
-      z2 += __shfl_xor_sync(0xffffffffu, z2, off);
-      n += __shfl_xor_sync(0xffffffffu, n, off);
-    }
-    if (lane < G) {
-#pragma unroll
-      for (int i = 0; i < N; ++i)
-        if (gl + i * G < A.E) sums[warp * A.E + gl + i * G] = acc[i];
+      for (int o = G; o < 32; o <<= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
+    for (int o = G; o < 32; o <<= 1) {
+      z2 += __shfl_xor_sync(0xffffffffu, z2, o);
+      n += __shfl_xor_sync(0xffffffffu, n, o);
     }
     if (lane == 0) {
       zs[warp] = z2;
       ns[warp] = n;
     }
+    float* row = sums + (warp % HALF) * A.E;
+    auto store = [&](bool add) {
+      if (lane >= G) return;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int e = expert<N, VEC>(i, gl, G);
+        if (e < A.E) row[e] = add ? row[e] + acc[i] : acc[i];
+      }
+    };
+    if (warp >= HALF) store(false);
+    __syncthreads();
+    if (warp < HALF) store(true);
     __syncthreads();
     const int64_t slot = (int64_t)blockIdx.x + r.s;
     for (int e = threadIdx.x; e < A.E; e += kThreads) {
       float s = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) s += sums[w * A.E + e];
+      for (int w = 0; w < HALF; ++w) s += sums[w * A.E + e];
       A.part_p[slot * A.E + e] = s;
       A.part_c[slot * A.E + e] = cnt[e];
     }
-    if (threadIdx.x == 0) {
-      float s = 0.f;
-      int c = 0;
-      for (int w = 0; w < kWarps; ++w) {
-        s += zs[w];
-        c += ns[w];
+    if (warp == kWarps - 1) {
+      const float s = warp_total(lane < kWarps ? zs[lane] : 0.f);
+      const int c = __reduce_add_sync(0xffffffffu, lane < kWarps ? ns[lane] : 0);
+      if (lane == 0) {
+        A.part_z[slot] = s;
+        A.part_n[slot] = c;
       }
-      A.part_z[slot] = s;
-      A.part_n[slot] = c;
     }
     __syncthreads();
     t = r.end;
@@ -229,11 +250,42 @@ struct Sums {  // outputs, and what the sequences leave for the last CTA
   int* arrived;
 };
 
-// A CTA adds up 32 experts of a sequence; the one that ends last adds up the losses.
-__global__ void __launch_bounds__(256) sequence_kernel(const __grid_constant__ Args A,
-                                                       const __grid_constant__ Sums B) {
-  __shared__ float sp[8][33], sz[8];
-  __shared__ int sc[8][33], sn[8];
+// Sums over a CTA's threads, in thread 0.
+template <int WARPS>
+struct BlockSum {
+  float f[2][WARPS];
+  int i[2][WARPS];
+  __device__ __forceinline__ void add(float& a, float& b, int& c, int& d) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    a = warp_total(a);
+    b = warp_total(b);
+    c = __reduce_add_sync(0xffffffffu, c);
+    d = __reduce_add_sync(0xffffffffu, d);
+    if (lane == 0) {
+      f[0][warp] = a;
+      f[1][warp] = b;
+      i[0][warp] = c;
+      i[1][warp] = d;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      a = warp_total(lane < WARPS ? f[0][lane] : 0.f);
+      b = warp_total(lane < WARPS ? f[1][lane] : 0.f);
+      c = __reduce_add_sync(0xffffffffu, lane < WARPS ? i[0][lane] : 0);
+      d = __reduce_add_sync(0xffffffffu, lane < WARPS ? i[1][lane] : 0);
+    }
+    __syncthreads();
+  }
+};
+
+// A CTA adds up 32 experts of a sequence; the one that ends last adds up the losses. WARPS: many for few
+// sequences, which have many slots.
+template <int WARPS>
+__global__ void __launch_bounds__(WARPS * 32) sequence_kernel(const __grid_constant__ Args A,
+                                                              const __grid_constant__ Sums B) {
+  __shared__ float sp[WARPS][33];
+  __shared__ int sc[WARPS][33];
+  __shared__ BlockSum<WARPS> all;
   __shared__ bool last;
   pdl_wait();
   pdl_trigger();
@@ -248,38 +300,30 @@ __global__ void __launch_bounds__(256) sequence_kernel(const __grid_constant__ A
   }
   const int64_t first = a / A.per_chunk + s;
   const int chunks = b > a ? (b - 1) / A.per_chunk - a / A.per_chunk + 1 : 0;
-  float p = 0.f, z = 0.f;
-  int c = 0, n = 0;
-#pragma unroll 4
-  for (int i = warp; i < chunks; i += 8) {
+  float p = 0.f, z = 0.f, none = 0.f;
+  int c = 0, n = 0, zero = 0;
+#pragma unroll 8
+  for (int i = warp; i < chunks; i += WARPS) {
     const int64_t slot = first + i;
     if (e < A.E) {
       p += A.part_p[slot * A.E + e];
       c += A.part_c[slot * A.E + e];
     }
   }
-  for (int i = threadIdx.x; i < chunks; i += 256) {
+  for (int i = threadIdx.x; i < chunks; i += WARPS * 32) {
     n += A.part_n[first + i];
     z += A.part_z[first + i];
   }
   sp[warp][lane] = p;
   sc[warp][lane] = c;
-  z = warp_total(z);
-  n = __reduce_add_sync(0xffffffffu, n);
-  if (lane == 0) {
-    sz[warp] = z;
-    sn[warp] = n;
-  }
-  __syncthreads();
+  all.add(z, none, n, zero);
   if (warp == 0) {
-    p = z = 0.f;
-    c = n = 0;
+    p = 0.f;
+    c = 0;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) {
+    for (int w = 0; w < WARPS; ++w) {
       p += sp[w][lane];
       c += sc[w][lane];
-      z += sz[w];
-      n += sn[w];
     }
     const float inv = n ? 1.f / (float)n : 0.f;
     p *= inv;
@@ -305,33 +349,15 @@ __global__ void __launch_bounds__(256) sequence_kernel(const __grid_constant__ A
   int some = 0;
   z = 0.f;
   n = 0;
-  for (int i = threadIdx.x; i < (int)gridDim.x; i += 256) loss += __ldcg(B.loss_part + i);
-  for (int i = threadIdx.x; i < A.S; i += 256) {
+  for (int i = threadIdx.x; i < (int)gridDim.x; i += WARPS * 32) loss += __ldcg(B.loss_part + i);
+  for (int i = threadIdx.x; i < A.S; i += WARPS * 32) {
     const int m = __ldcg(B.tokens + i);
     z += __ldcg(B.z_part + i);
     n += m;
     some += m > 0;
   }
-  loss = warp_total(loss);
-  z = warp_total(z);
-  n = __reduce_add_sync(0xffffffffu, n);
-  some = __reduce_add_sync(0xffffffffu, some);
-  if (lane == 0) {
-    sp[warp][0] = loss;
-    sp[warp][1] = z;
-    sc[warp][0] = n;
-    sc[warp][1] = some;
-  }
-  __syncthreads();
+  all.add(loss, z, n, some);
   if (threadIdx.x == 0) {
-    loss = z = 0.f;
-    n = some = 0;
-    for (int w = 0; w < 8; ++w) {
-      loss += sp[w][0];
-      z += sp[w][1];
-      n += sc[w][0];
-      some += sc[w][1];
-    }
     B.losses[0] = some ? loss / (float)some : 0.f;
     B.losses[1] = n ? z / (float)n : 0.f;
     B.totals[0] = some;
@@ -340,76 +366,86 @@ __global__ void __launch_bounds__(256) sequence_kernel(const __grid_constant__ A
 }
 
 // The gradient: the same walk over the tokens, a sequence's weights in registers.
-template <int N>
-__global__ void __launch_bounds__(256) backward_kernel(const __grid_constant__ Args A,
-                                                       const float* __restrict__ dlosses,
-                                                       const int32_t* __restrict__ counts,
-                                                       const int32_t* __restrict__ tokens,
-                                                       const int32_t* __restrict__ totals, int add,
-                                                       float* __restrict__ dlogits) {
+template <int N, bool VEC, bool SIGMOID>
+__global__ void __launch_bounds__(kBackThreads) backward_kernel(
+    const __grid_constant__ Args A, const float* __restrict__ dlosses,
+    const int32_t* __restrict__ counts, const int32_t* __restrict__ tokens,
+    const int32_t* __restrict__ totals, int add, float* __restrict__ dlogits) {
+  __shared__ Offsets off;
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31;
-  const int G = A.group, gl = lane & (G - 1), at_once = 256 / G, sub = threadIdx.x / G;
+  const int G = A.group, gl = lane & (G - 1), groups = kBackThreads / G, sub = threadIdx.x / G;
   const int t0 = blockIdx.x * A.per_chunk, t1 = min(A.T, t0 + A.per_chunk);
   const int some = __ldg(totals), all = __ldg(totals + 1);
   const float d0 = __ldg(dlosses), d1 = __ldg(dlosses + 1) * 2.f / (float)max(all, 1);
-  float bias[N];
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int e = gl + i * G;
-    bias[i] = A.bias && e < A.E ? __ldg(A.bias + e) : 0.f;
-  }
+  off.fetch(A);
   for (int t = t0; t < t1;) {
-    const Run r = run_of(A, t, t1);
-    float g[N];
+    const Run r = off.run(A, t, t1);
+    float f = 0.f, g[N];
     if (r.s >= 0) {
       const float n = (float)max(__ldg(tokens + r.s), 1);
-      const float f = d0 * ((float)A.E / (float)A.k) / (n * n * (float)max(some, 1));
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const int e = gl + i * G;
-        g[i] = e < A.E ? f * (float)__ldg(counts + (int64_t)r.s * A.E + e) : 0.f;
-      }
+      f = d0 * ((float)A.E / (float)A.k) / (n * n * (float)max(some, 1));
     }
-    for (int b = t; b < r.end; b += at_once) {
+    load_lane<N, VEC>((const float*)counts + (int64_t)max(r.s, 0) * A.E, r.s >= 0, A.E, gl, G, 0.f, g);
+#pragma unroll
+    for (int i = 0; i < N; ++i) g[i] = f * (float)__float_as_int(g[i]);
+    for (int b = t; b < r.end; b += groups) {
       const int64_t mine = (int64_t)b + sub;
-      const bool in = mine < r.end, live = in && r.s >= 0 && (!A.mask || A.mask[mine]);
-      float z[N], d[N];
-      load_logits<N>(A, mine, live, gl, z);
-      if (add) {
+      const bool in = mine < r.end;
+      float z[N];
+      load_lane<N, VEC>(A.logits + mine * A.E, in && r.s >= 0, A.E, gl, G, -INFINITY, z);
+      const bool live = in && r.s >= 0 && (!A.mask || A.mask[mine]);
+      if (A.bias) {
+        float bias[N];
+        load_lane<N, VEC>(A.bias, true, A.E, gl, G, 0.f, bias);
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-          d[i] = live && gl + i * G < A.E ? dlogits[mine * A.E + gl + i * G] : 0.f;
+        for (int i = 0; i < N; ++i) z[i] += bias[i];
       }
-#pragma unroll
-      for (int i = 0; i < N; ++i) z[i] += bias[i];
-      Token<N> k;
-      k.set(z, G, A.sigmoid);
+      Token<N, SIGMOID> k;
+      k.set(z, G);
       float dot = 0.f;
-      if (r.s >= 0) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) dot = fmaf(g[i], k.p[i], dot);
-      }
+      for (int i = 0; i < N; ++i) dot = fmaf(g[i], k.p[i], dot);
       dot = group_add(dot, G);
       const float dl = d1 * k.lse;
       if (!in || (add && !live)) continue;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        if (gl + i * G >= A.E) continue;
-        float v = live ? fmaf(k.p[i] * k.slope[i], g[i] - dot, dl * k.soft[i]) : 0.f;
-        if (add) v += d[i];
-        dlogits[mine * A.E + gl + i * G] = v;
+        if constexpr (SIGMOID) z[i] = fmaf(k.p[i] * k.slope[i], g[i] - dot, dl * k.soft[i]);
+        else z[i] = k.p[i] * (g[i] - dot + dl);
+        if (!live) z[i] = 0.f;
+      }
+      float* row = dlogits + mine * A.E;
+      if constexpr (VEC) {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+          const int e = expert<N, VEC>(i, gl, G);
+          if (e >= A.E) break;
+          float4 v = make_float4(z[i], z[i + 1], z[i + 2], z[i + 3]);
+          if (add) {
+            const float4 o = *(const float4*)(row + e);
+            v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
+          }
+          *(float4*)(row + e) = v;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const int e = expert<N, VEC>(i, gl, G);
+          if (e < A.E) row[e] = add ? row[e] + z[i] : z[i];
+        }
       }
     }
     t = r.end;
   }
 }
 
-// Lanes of a token and experts a lane.
+// Experts of a lane at most, and lanes of a token.
+static int per_lane(int E) { return E <= 4 ? 4 : E <= 8 ? 8 : 16; }
 static int group_of(int E) {
   int g = 1;
-  while (g < 32 && g < E) g <<= 1;
+  while (g * per_lane(E) < E) g <<= 1;
   return g;
 }
 static Args args_of(const moe_balance_t& c, const float* logits, int ctas, int threads) {
@@ -429,12 +465,14 @@ static Args args_of(const moe_balance_t& c, const float* logits, int ctas, int t
   A.per_chunk = std::max(threads / A.group, ceil_div(c.T, ctas));
   return A;
 }
-static int forward_ctas() { return num_sms() * 2; }
+static Args forward_args(const moe_balance_t& c, const float* logits) {
+  return args_of(c, logits, num_sms() * 2, kThreads);
+}
 struct Layout {
   size_t p, c, n, z, loss, zs, arrived, total;
 };
 static Layout layout(const moe_balance_t& c) {
-  const Args A = args_of(c, nullptr, forward_ctas(), kThreads);
+  const Args A = forward_args(c, nullptr);
   const size_t slots = (size_t)ceil_div(A.T, A.per_chunk) + A.S;
   Layout l{};
   size_t at = 0;
@@ -454,12 +492,14 @@ static Layout layout(const moe_balance_t& c) {
   return l;
 }
 
-#define BALANCE_PICK(name)                    \
-  (c.E <= 32    ? go(name<1>)                 \
-   : c.E <= 64  ? go(name<2>)                 \
-   : c.E <= 128 ? go(name<4>)                 \
-   : c.E <= 256 ? go(name<8>)                 \
-                : go(name<16>))
+// The kernel instance of a configuration; rows in pieces of four where they are aligned.
+#define BALANCE_PICK_N(name, V, S) (c.E <= 4 ? go(name<4, V, S>) : c.E <= 8 ? go(name<8, V, S>) : go(name<16, V, S>))
+#define BALANCE_PICK(name, vec)                                                            \
+  (A.sigmoid ? (vec ? BALANCE_PICK_N(name, true, true) : BALANCE_PICK_N(name, false, true)) \
+             : (vec ? BALANCE_PICK_N(name, true, false) : BALANCE_PICK_N(name, false, false)))
+static bool pieces(const Args& A, const void* a, const void* b) {
+  return A.E % 4 == 0 && (((uintptr_t)A.logits | (uintptr_t)A.bias | (uintptr_t)a | (uintptr_t)b) & 15) == 0;
+}
 
 }  // namespace balance
 
@@ -470,7 +510,7 @@ size_t balance_ws_bytes(const moe_balance_t& c) { return layout(c).total; }
 moe_status_t launch_balance(const moe_balance_t& c, const float* logits, const int32_t* ids,
                             float* losses, int32_t* counts, int32_t* tokens, float* prob,
                             int32_t* totals, void* ws, cudaStream_t s) {
-  Args A = args_of(c, logits, forward_ctas(), kThreads);
+  Args A = forward_args(c, logits);
   const Layout l = layout(c);
   uint8_t* w = (uint8_t*)ws;
   A.ids = ids;
@@ -480,24 +520,26 @@ moe_status_t launch_balance(const moe_balance_t& c, const float* logits, const i
   A.part_z = (float*)(w + l.z);
   Sums B{losses, prob, counts, tokens, totals, (float*)(w + l.loss), (float*)(w + l.zs), (int*)(w + l.arrived)};
   auto go = [&](auto kern) {
-    return launch_k(kern, dim3(ceil_div(c.T, A.per_chunk)), dim3(kThreads),
-                    (size_t)kWarps * c.E * sizeof(float), s, (const Args&)A, B.arrived);
+    return launch_k(kern, dim3(ceil_div(c.T, A.per_chunk)), dim3(kThreads), 0, s, (const Args&)A, B.arrived);
   };
-  const moe_status_t st = BALANCE_PICK(partial_kernel);
+  const moe_status_t st = BALANCE_PICK(partial_kernel, pieces(A, nullptr, nullptr));
   if (st != MOE_OK) return st;
-  return launch_k(sequence_kernel, dim3(A.S * ceil_div(c.E, 32)), dim3(256), 0, s, (const Args&)A, (const Sums&)B);
+  const int blocks = A.S * ceil_div(c.E, 32);
+  if (blocks <= 2 * num_sms())
+    return launch_k(sequence_kernel<32>, dim3(blocks), dim3(1024), 0, s, (const Args&)A, (const Sums&)B);
+  return launch_k(sequence_kernel<4>, dim3(blocks), dim3(128), 0, s, (const Args&)A, (const Sums&)B);
 }
 
 moe_status_t launch_balance_backward(const moe_balance_t& c, const float* dlosses,
                                      const float* logits, const int32_t* counts,
                                      const int32_t* tokens, const int32_t* totals, int accumulate,
                                      float* dlogits, cudaStream_t s) {
-  const Args A = args_of(c, logits, num_sms() * 4, 256);
+  const Args A = args_of(c, logits, num_sms() * 4, kBackThreads);
   auto go = [&](auto kern) {
-    return launch_k(kern, dim3(ceil_div(c.T, A.per_chunk)), dim3(256), 0, s, A, dlosses, counts, tokens,
+    return launch_k(kern, dim3(ceil_div(c.T, A.per_chunk)), dim3(kBackThreads), 0, s, A, dlosses, counts, tokens,
                     totals, accumulate, dlogits);
   };
-  return BALANCE_PICK(backward_kernel);
+  return BALANCE_PICK(backward_kernel, pieces(A, counts, dlogits));
 }
 
 int balance_status_read(int reset) {
