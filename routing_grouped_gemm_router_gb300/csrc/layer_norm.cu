@@ -24,19 +24,9 @@ namespace lnorm {
 using namespace rows;
 
 // ------------------------------------------------------------------- forward
-// Elements that warp `w` of a row's group holds.
-template <int VPT>
-__device__ __forceinline__ float warp_elements(const Shape& S, int w) {
-  int n = 0;
-#pragma unroll
-  for (int v = 0; v < VPT; ++v) n += min(max(S.chunks - (w * 32 + v * S.group), 0), 32);
-  return 8.f * n;
-}
-
 // Keeps or drops eight elements and scales them: y * factor, or 0 whatever y is.
 template <bool DROP>
-__device__ __forceinline__ void drop_scale(F2 (&y)[4], const Philox* rng, const Drop& d,
-                                           int64_t first) {
+__device__ __forceinline__ void drop_scale(F2 (&y)[4], Philox* rng, const Drop& d, int64_t first) {
   if (DROP) {
     uint32_t w[8];
     rng->eight(first, w);
@@ -52,123 +42,130 @@ __device__ __forceinline__ void drop_scale(F2 (&y)[4], const Philox* rng, const 
   }
 }
 
-// JOIN: out = x + scale dropout(y), then (if gamma) its norm; otherwise the norm of x. Row tensors: JOIN y,
-// x; otherwise x.
-template <typename T, int VPT, int THREADS, bool JOIN, bool DROP>
-__global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 4 / VPT + 1 : 1)
-    forward_kernel(const __grid_constant__ Shape S, const __grid_constant__ LayerArgs A) {
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ Reducer red;
-  const int local = threadIdx.x / S.group, g = threadIdx.x - local * S.group;
-  const int lane = threadIdx.x & 31, warps = S.group >> 5;
-  Ring<T, VPT, 2> ring(S, smem, local, g);
-  const float inv_mine = 1.f / fmaxf(warp_elements<VPT>(S, g >> 5), 1.f);
-  const float n_lane = lane < warps ? warp_elements<VPT>(S, lane) : 0.f;
-  const float inv_lane = 1.f / fmaxf(n_lane, 1.f);
+// Rows of the forward kernel: `warps` warps a row, chunk c of the row held by thread c % (32 warps); several
+// rows a CTA where one warp takes a row.
+struct Rows {
+  int T, H, chunks, warps;
+  float eps, inv_h;
+};
+
+// JOIN: out = x + scale dropout(y), then (if gamma) its norm; otherwise the norm of x. A row's elements are all
+// asked for at once and stay in registers, and a CTA is done after its row: with many small CTAs an SM has
+// enough rows in flight to hide the chain of a row's reductions. (With persistent CTAs and the
+// rings of the backward kernels three rows an SM were in flight, and 8192 rows of 4096 took 36 us.)
+template <typename T, int VPT, bool JOIN, bool DROP>
+__global__ void __launch_bounds__(512) forward_kernel(const __grid_constant__ Rows R,
+                                                      const __grid_constant__ LayerArgs A) {
+  __shared__ float near_mean[16], near_m2[16];
+  const int group = R.warps * 32, local = threadIdx.x / group, g = threadIdx.x - local * group;
+  const int64_t t = (int64_t)blockIdx.x * (blockDim.x / group) + local;
   pdl_wait();
   pdl_trigger();
-  ring.start();
+  if (t >= R.T) return;  // a warp with a row of its own
+  const int64_t row = t * R.H;
+  const uint8_t* from = (const uint8_t*)(JOIN ? A.y : A.x) + row * sizeof(T);
+  const uint8_t* from_x = (const uint8_t*)A.x + row * sizeof(T);
+  Chunk<T> q[VPT], xq[JOIN ? VPT : 1];
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    const int c = g + v * group;
+    if (c >= R.chunks) break;
+    q[v].load(from + c * Chunk<T>::kBytes);
+    if (JOIN) xq[v].load(from_x + c * Chunk<T>::kBytes);
+  }
   Philox rng = DROP ? Philox(A.drop) : Philox();
-  int turn = 0;
-  for (int u = blockIdx.x; u < S.units; u += gridDim.x) {
-    const int t = u * S.per + local;
-    const bool live = t < S.T;
-    const int tl = live ? t : 0;
-    const int64_t row = (int64_t)tl * S.H;
-    ring.wait();
-    F2 o[VPT][4], s = dup(0.f);
+  F2 o[VPT][4], s = dup(0.f);
 #pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-      const int c = g + v * S.group;
-      if (!ring.has[v] || !live) continue;
-      Chunk<T> q;
-      ring.get(q, 0, v, tl);
-      q.get(o[v]);
-      if (JOIN) {
-        drop_scale<DROP>(o[v], &rng, A.drop, row + c * 8);
-        Chunk<T> xq;
-        F2 x[4];
-        ring.get(xq, 1, v, tl);
-        xq.get(x);
+  for (int v = 0; v < VPT; ++v) {
+    const int c = g + v * group;
+    if (c >= R.chunks) break;
+    q[v].get(o[v]);
+    if (JOIN) {
+      drop_scale<DROP>(o[v], &rng, A.drop, row + c * 8);
+      F2 x[4];
+      xq[v].get(x);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[v][i] = o[v][i] + x[i];
-        q.set(o[v]);
-        q.store(A.out, row + c * 8);
-        q.get(o[v]);  // the norm reads what is stored
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s = s + o[v][i];
+      for (int i = 0; i < 4; ++i) o[v][i] = o[v][i] + x[i];
+      Chunk<T> out;
+      out.set(o[v]);
+      out.store(A.out, row + c * 8);
+      out.get(o[v]);  // the norm reads what is stored
     }
-    const float sum = warp_total(both(s));
-    ring.refill(u);
-    if (JOIN && !A.gamma) continue;
-    const F2 near = dup(-sum * inv_mine);
-    s = dup(0.f);
 #pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-      if (!ring.has[v] || !live) continue;
+    for (int i = 0; i < 4; ++i) s = s + o[v][i];
+  }
+  if (JOIN && !A.gamma) return;
+  // a warp's own mean, and the sum of squares about it
+  const int full = R.chunks / group * 256, rest = R.chunks % group * 8;
+  auto elements = [&](int w) { return (float)(full + min(max(rest - w * 256, 0), 256)); };
+  float mean = warp_total(both(s)) / fmaxf(elements(g >> 5), 1.f);
+  const F2 near = dup(-mean);
+  s = dup(0.f);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const F2 d = o[v][i] + near;
-        s = fma2(d, d, s);
-      }
-    }
-    float m2 = warp_total(both(s)), mean = sum * S.inv_h;
-    if (warps > 1) {
-      auto& buf = red.buf[turn];
-      turn ^= 1;
-      const int w = threadIdx.x >> 5, first = w - (g >> 5);
-      if (lane == 0) {
-        buf[0][w] = sum;
-        buf[1][w] = m2;
-      }
-      __syncthreads();
-      const float sw = lane < warps ? buf[0][first + lane] : 0.f;
-      mean = warp_total(sw) * S.inv_h;
-      const float off = sw * inv_lane - mean;
-      m2 = warp_total(lane < warps ? fmaf(n_lane * off, off, buf[1][first + lane]) : 0.f);
-    }
-    if (!live) continue;
-    const float r = rsqrtf(m2 * S.inv_h + S.eps);
-    if (g == 0) {
-      A.mean[t] = mean;
-      A.rstd[t] = r;
-    }
-    const F2 rr = dup(r), mm = dup(-mean);
+  for (int v = 0; v < VPT; ++v) {
+    if (g + v * group >= R.chunks) break;
 #pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-      const int c = g + v * S.group;
-      if (!ring.has[v]) continue;
-      F2 ga[4], be[4];
-      load_w(A.gamma, c * 8, ga);
-      if (A.beta) load_w(A.beta, c * 8, be);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const F2 xn = (o[v][i] + mm) * rr;
-        ga[i] = A.beta ? fma2(xn, ga[i], be[i]) : xn * ga[i];
-      }
-      Chunk<T> q;
-      q.set(ga);
-      q.store(A.h, row + c * 8);
+    for (int i = 0; i < 4; ++i) {
+      const F2 d = o[v][i] + near;
+      s = fma2(d, d, s);
     }
+  }
+  float m2 = warp_total(both(s));
+  if (R.warps > 1) {
+    if ((threadIdx.x & 31) == 0) {
+      near_mean[g >> 5] = mean;
+      near_m2[g >> 5] = m2;
+    }
+    __syncthreads();
+    mean = m2 = 0.f;
+    for (int w = 0; w < R.warps; ++w) mean = fmaf(elements(w) * R.inv_h, near_mean[w], mean);
+    for (int w = 0; w < R.warps; ++w) {
+      const float off = near_mean[w] - mean;
+      m2 += fmaf(elements(w) * off, off, near_m2[w]);
+    }
+  }
+  const float r = rsqrtf(m2 * R.inv_h + R.eps);
+  if (g == 0) {
+    A.mean[t] = mean;
+    A.rstd[t] = r;
+  }
+  const F2 rr = dup(r), mm = dup(-mean);
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    const int c = g + v * group;
+    if (c >= R.chunks) break;
+    F2 ga[4], be[4];
+    load_w(A.gamma, c * 8, ga);
+    if (A.beta) load_w(A.beta, c * 8, be);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const F2 xn = (o[v][i] + mm) * rr;
+      ga[i] = A.beta ? fma2(xn, ga[i], be[i]) : xn * ga[i];
+    }
+    Chunk<T> h;
+    h.set(ga);
+    h.store(A.h, row + c * 8);
   }
 }
 
 // ------------------------------------------------------------------- backward
-// JOIN: dy too. RES: dres is there. Row tensors: dh, x, (dres).
-template <typename T, int VPT, int THREADS, bool JOIN, bool DROP, bool RES>
+// JOIN: dy too. Row tensors: dh, x, (dres). A group takes ROWS rows at a time, whose sums meet at one barrier
+// and whose weights are loaded once; dh and x stay in registers as they are stored, dres is read from
+// the ring when the sums are there.
+template <typename T, int VPT, int THREADS, int ROWS, bool JOIN, bool DROP>
 __global__ void __launch_bounds__(THREADS, VPT <= 2 && THREADS <= 256 ? 2 : 1)
     backward_kernel(const __grid_constant__ Shape S, const __grid_constant__ LayerArgs A, int kinds,
                     const Outs outs) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Reducer red;
   const int local = threadIdx.x / S.group, g = threadIdx.x - local * S.group;
-  Ring<T, VPT, 3> ring(S, smem, local, g);
+  Ring<T, VPT, 3, ROWS> ring(S, smem, local, g);
   pdl_wait();
   pdl_trigger();
   ring.start();
   Philox rng = DROP ? Philox(A.drop) : Philox();
   int turn = 0;
+  const bool res = A.dres;
   const F2 zero = dup(0.f);
   F2 sg[VPT][4], sb[VPT][4];
 #pragma unroll
@@ -176,137 +173,192 @@ __global__ void __launch_bounds__(THREADS, VPT <= 2 && THREADS <= 256 ? 2 : 1)
 #pragma unroll
     for (int i = 0; i < 4; ++i) sg[v][i] = sb[v][i] = zero;
 
-  // a row's scalars are asked for one row ahead: nothing else hides their way from L2
-  float m_next = 0.f, r_next = 0.f;
-  auto scalars = [&](int64_t t) {
-    if (t >= S.T) t = 0;
-    m_next = __ldg(A.mean_in + t);
-    r_next = __ldg(A.rstd_in + t);
+  // a row's scalars are asked for one unit ahead: nothing else hides their way from L2
+  float m_next[ROWS], r_next[ROWS];
+  auto scalars = [&](int64_t u) {
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      int64_t t = (u * S.per + local) * ROWS + r;
+      if (t >= S.T) t = 0;
+      m_next[r] = __ldg(A.mean_in + t);
+      r_next[r] = __ldg(A.rstd_in + t);
+    }
   };
-  scalars((int64_t)blockIdx.x * S.per + local);
+  scalars(blockIdx.x);
+  F2 w[VPT][4];
+#pragma unroll
+  for (int v = 0; v < VPT; ++v)
+    if (ring.has[v]) load_w(A.gamma, (g + v * S.group) * 8, w[v]);
   for (int u = blockIdx.x; u < S.units; u += gridDim.x) {
-    const int t = u * S.per + local;
-    const bool live = t < S.T;
-    const int tl = live ? t : 0;
-    const int64_t row = (int64_t)tl * S.H;
-    const float r = r_next;
-    const F2 rr = dup(r), shift = dup(-m_next * r);  // xn = x r + shift
-    const F2 mm = dup(-m_next);
-    scalars((int64_t)t + (int64_t)gridDim.x * S.per);
+    const int t0 = (u * S.per + local) * ROWS;
+    F2 rr[ROWS], mm[ROWS];
+    float rstd[ROWS];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      rstd[r] = r_next[r];
+      rr[r] = dup(rstd[r]);
+      mm[r] = dup(-m_next[r]);
+    }
+    scalars((int64_t)u + gridDim.x);
     ring.wait();
-    Chunk<T> xq[VPT];
-    F2 d[VPT][4], s1 = zero, s2 = zero;
+    Chunk<T> xq[ROWS][VPT], dq[ROWS][VPT];
+    F2 s1[ROWS], s2[ROWS];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) s1[r] = s2[r] = zero;
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      if (!ring.has[v]) continue;
+      const F2(&ga)[4] = w[v];
+#pragma unroll
+      for (int r = 0; r < ROWS; ++r) {
+        if (t0 + r >= S.T) continue;
+        ring.get(dq[r][v], 0, v, t0 + r, r);
+        ring.get(xq[r][v], 1, v, t0 + r, r);
+        F2 x[4], d[4];
+        dq[r][v].get(d);
+        xq[r][v].get(x);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const F2 xn = (x[i] + mm[r]) * rr[r];
+          sg[v][i] = fma2(d[i], xn, sg[v][i]);
+          sb[v][i] = sb[v][i] + d[i];
+          d[i] = d[i] * ga[i];
+          s1[r] = fma2(d[i], xn, s1[r]);
+          s2[r] = s2[r] + d[i];
+        }
+      }
+    }
+    float s[2 * ROWS];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      s[2 * r] = both(s1[r]);
+      s[2 * r + 1] = both(s2[r]);
+    }
+    group_sum<2 * ROWS>(s, S.group, red, turn);
+    // dx = dres + r (a - mean(a) - mean(a xn) xn)
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
       const int c = g + v * S.group;
-      if (!ring.has[v] || !live) continue;
-      Chunk<T> q;
-      F2 x[4], ga[4];
-      ring.get(q, 0, v, tl);
-      ring.get(xq[v], 1, v, tl);
-      q.get(d[v]);
-      xq[v].get(x);
-      load_w(A.gamma, c * 8, ga);
+      if (!ring.has[v]) continue;
+      const F2(&ga)[4] = w[v];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const F2 xn = (x[i] + mm) * rr;
-        sg[v][i] = fma2(d[v][i], xn, sg[v][i]);
-        sb[v][i] = sb[v][i] + d[v][i];
-        d[v][i] = d[v][i] * ga[i];
-        s1 = fma2(d[v][i], xn, s1);
-        s2 = s2 + d[v][i];
-      }
-      if (RES) {
-        F2 f[4];
-        ring.get(q, 2, v, tl);
-        q.get(f);
+      for (int r = 0; r < ROWS; ++r) {
+        if (t0 + r >= S.T) continue;
+        const F2 m1 = dup(-s[2 * r] * S.inv_h), m0 = dup(-s[2 * r + 1] * S.inv_h);
+        const int64_t at = (int64_t)(t0 + r) * S.H + c * 8;
+        F2 x[4], d[4];
+        dq[r][v].get(d);
+        xq[r][v].get(x);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) d[v][i] = fma2(d[v][i], rr, f[i]);
-      } else {
+        for (int i = 0; i < 4; ++i) {
+          const F2 xn = (x[i] + mm[r]) * rr[r];
+          d[i] = fma2(xn, m1, fma2(d[i], ga[i], m0));
+        }
+        Chunk<T> o;
+        if (res) {
+          F2 f[4];
+          ring.get(o, 2, v, t0 + r, r);
+          o.get(f);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) d[v][i] = d[v][i] * rr;
+          for (int i = 0; i < 4; ++i) d[i] = fma2(d[i], rr[r], f[i]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) d[i] = d[i] * rr[r];
+        }
+        o.set(d);
+        o.store(A.dx, at);
+        if (JOIN) {
+          drop_scale<DROP>(d, &rng, A.drop, at);
+          o.set(d);
+          o.store(A.dy, at);
+        }
       }
     }
-    float s[2] = {both(s1), both(s2)};
-    group_sum<2>(s, S.group, red, turn);
     ring.refill(u);
-    // dx = d - r mean(a) - r mean(a xn) xn
-    const F2 m1 = dup(-s[0] * S.inv_h * r), m0 = dup(-s[1] * S.inv_h * r);
-#pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-      const int c = g + v * S.group;
-      if (!ring.has[v] || !live) continue;
-      F2 x[4];
-      xq[v].get(x);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) d[v][i] = fma2((x[i] + mm) * rr, m1, d[v][i] + m0);
-      Chunk<T> o;
-      o.set(d[v]);
-      o.store(A.dx, row + c * 8);
-      if (JOIN) {
-        drop_scale<DROP>(d[v], &rng, A.drop, row + c * 8);
-        o.set(d[v]);
-        o.store(A.dy, row + c * 8);
-      }
-    }
   }
   leave_columns<VPT>(S, smem, local, g, sg, 0, kinds, 1.f, A.ws, outs);
   if (kinds > 1) leave_columns<VPT>(S, smem, local, g, sb, 1, kinds, 1.f, A.ws, outs);
 }
 
-// Chunks of 8 elements a thread holds: as many as it takes for a row to have at most 256 threads (bf16,
-// up to 8192 channels) or 448 (fp32, up to 7168, where more chunks would not fit the ring), and twice as
-// many threads or chunks beyond. The backward kernels hold 24 registers of sums and gradients a chunk, so
-// a row's threads are capped where the chunks are counted.
-static int vec_of(const moe_layer_t& c) {
+// Chunks of 8 elements a thread holds. Backward, two: the sums over tokens take 16 registers a chunk.
+static int wide(const moe_layer_t& c) {
   const int chunks = c.H / 8;
-  if (c.dtype == MOE_F32) return chunks <= 32 ? 1 : chunks <= 896 ? 2 : chunks <= 2048 ? 4 : 8;
-  return chunks <= 32 ? 1 : chunks <= 512 ? 2 : chunks <= 2048 ? 4 : 8;
+  const int two = c.dtype == MOE_F32 ? 896 : 1024;
+  return chunks <= 32 ? 1 : chunks <= two ? 2 : chunks <= 2048 ? 4 : 8;
 }
-static Shape shape_of(const moe_layer_t& c) {
+// Forward, up to eight (fp32: four), so that few warps share a row's reductions; with few rows for an SM as
+// few as give a row 512 threads at most: one row's latency counts.
+static int narrow(const moe_layer_t& c) {
+  const int chunks = c.H / 8;
+  if (c.T < 4 * num_sms()) return chunks <= 32 ? 1 : chunks <= 1024 ? 2 : chunks <= 2048 ? 4 : 8;
+  if (c.dtype == MOE_F32 && chunks <= 2048) return chunks <= 32 ? 1 : chunks <= 64 ? 2 : 4;
+  return chunks <= 32 ? 1 : chunks <= 64 ? 2 : chunks <= 128 ? 4 : 8;
+}
+static Shape shape_of(const moe_layer_t& c, int vec, int rows) {
   Shape s{};
   s.T = c.T;
   s.H = c.H;
   s.chunks = c.H / 8;
-  s.group = ceil_div(ceil_div(s.chunks, vec_of(c)), 32) * 32;
-  s.per = std::min(c.T, std::max(1, 256 / s.group));
-  s.units = ceil_div(c.T, s.per);
+  s.group = ceil_div(ceil_div(s.chunks, vec), 32) * 32;
+  s.rows = rows;
+  s.per = std::min(ceil_div(c.T, rows), std::max(1, 256 / s.group));
+  s.units = ceil_div(c.T, s.per * rows);
   s.scale = c.scale;
   s.eps = c.eps;
   s.inv_h = 1.0f / (float)c.H;
   return s;
 }
+// Rows that a group takes at a time in the backward kernels: two of bf16, where that leaves every SM work.
+static int rows_of(const moe_layer_t& c) {
+  if (c.dtype != MOE_BF16 || c.H > 8192) return 1;
+  return shape_of(c, wide(c), 2).units >= 2 * num_sms() ? 2 : 1;
+}
 
 using bf = __nv_bfloat16;
 
-// The kernel instance of a dtype and a row length.
-#define LNORM_PICK(name, ...)                                                                 \
-  (c.dtype == MOE_BF16 ? (v == 1   ? go(name<bf, 1, 256, __VA_ARGS__>)                        \
-                          : v == 2 ? go(name<bf, 2, 256, __VA_ARGS__>)                        \
-                          : v == 4 ? (c.H <= 8192 ? go(name<bf, 4, 256, __VA_ARGS__>)         \
-                                                  : go(name<bf, 4, 512, __VA_ARGS__>))        \
-                                   : go(name<bf, 8, 512, __VA_ARGS__>))                       \
-                       : (v == 1   ? go(name<float, 1, 256, __VA_ARGS__>)                     \
-                          : v == 2 ? go(name<float, 2, 448, __VA_ARGS__>)                     \
-                          : v == 4 ? go(name<float, 4, 512, __VA_ARGS__>)                     \
-                                   : go(name<float, 8, 512, __VA_ARGS__>)))
-
-template <bool JOIN, bool DROP>
-static moe_status_t forward(const moe_layer_t& c, const LayerArgs& a, cudaStream_t s) {
-  Shape S = shape_of(c);
-  if (JOIN) S.in[S.n_in++] = a.y;
-  S.in[S.n_in++] = a.x;
-  int blocks = 0;
-  const int v = vec_of(c);
-  auto go = [&](auto kern) {
-    return run(kern, S, dtype_size(c.dtype), 0, v * dtype_size(c.dtype) <= 8, 8, blocks, s, a);
-  };
-  return LNORM_PICK(forward_kernel, JOIN, DROP);
+// Calls f with the instance of a dtype and a row length: element type, chunks and threads.
+template <typename T_, int VPT, int THREADS>
+struct Instance {
+  using T = T_;
+  static constexpr int vpt = VPT, threads = THREADS;
+};
+template <typename T, typename F>
+static moe_status_t pick(int vec, int group, F f) {
+  if (vec == 1) return f(Instance<T, 1, 256>{});
+  if (vec == 2) return group <= 256 ? f(Instance<T, 2, 256>{}) : group <= 448 ? f(Instance<T, 2, 448>{}) : f(Instance<T, 2, 512>{});
+  if (vec == 4) return group <= 256 ? f(Instance<T, 4, 256>{}) : f(Instance<T, 4, 512>{});
+  return group <= 256 ? f(Instance<T, 8, 256>{}) : f(Instance<T, 8, 512>{});
+}
+template <typename F>
+static moe_status_t pick(const moe_layer_t& c, int vec, int group, F f) {
+  return c.dtype == MOE_BF16 ? pick<bf>(vec, group, f) : pick<float>(vec, group, f);
 }
 
 template <bool JOIN, bool DROP>
+static moe_status_t forward(const moe_layer_t& c, const LayerArgs& a, cudaStream_t s) {
+  const int v = narrow(c);
+  Rows R{c.T, c.H, c.H / 8, ceil_div(c.H / 8, 32 * v), c.eps, 1.0f / (float)c.H};
+  const int per = R.warps == 1 ? 4 : 1;
+  auto go = [&](auto kern) {
+    return launch_k(kern, dim3(ceil_div(c.T, per)), dim3(R.warps * 32 * per), 0, s, (const Rows&)R, a);
+  };
+  if (c.dtype == MOE_BF16)
+    return v == 1   ? go(forward_kernel<bf, 1, JOIN, DROP>)
+           : v == 2 ? go(forward_kernel<bf, 2, JOIN, DROP>)
+           : v == 4 ? go(forward_kernel<bf, 4, JOIN, DROP>)
+                    : go(forward_kernel<bf, 8, JOIN, DROP>);
+  return v == 1   ? go(forward_kernel<float, 1, JOIN, DROP>)
+         : v == 2 ? go(forward_kernel<float, 2, JOIN, DROP>)
+         : v == 4 ? go(forward_kernel<float, 4, JOIN, DROP>)
+                  : go(forward_kernel<float, 8, JOIN, DROP>);
+}
+
+// Bytes of rows in flight an SM in the backward kernels: with two rows a group, two stages of two CTAs.
+constexpr size_t kBackBudget = 200 * 1024;
+
+template <bool JOIN, bool DROP>
 static moe_status_t backward(const moe_layer_t& c, const LayerArgs& a, cudaStream_t s) {
-  Shape S = shape_of(c);
+  Shape S = shape_of(c, wide(c), rows_of(c));
   S.in[S.n_in++] = a.dh;
   S.in[S.n_in++] = a.x;
   if (a.dres) S.in[S.n_in++] = a.dres;
@@ -317,13 +369,17 @@ static moe_status_t backward(const moe_layer_t& c, const LayerArgs& a, cudaStrea
   // the CTA's groups meet in shared memory at the end
   const size_t least = S.per > 1 ? (size_t)S.per * S.H * sizeof(float) : 0;
   int blocks = 0;
-  const int v = vec_of(c);
-  auto go = [&](auto kern) {
-    return run(kern, S, dtype_size(c.dtype), least, v * dtype_size(c.dtype) <= 8, kMaxCtas, blocks, s, a,
-               kinds, outs);
-  };
-  const moe_status_t st = a.dres ? LNORM_PICK(backward_kernel, JOIN, DROP, true)
-                                 : LNORM_PICK(backward_kernel, JOIN, DROP, false);
+  const moe_status_t st = pick(c, wide(c), S.group, [&](auto i) {
+    using I = decltype(i);
+    using T = typename I::T;
+    auto go = [&](auto kern) {
+      return run_within(kBackBudget, kern, S, sizeof(T), least, kRinged<T, I::vpt>, kMaxCtas, blocks, s, a, kinds,
+                        outs);
+    };
+    if constexpr (sizeof(T) == 2 && I::vpt <= 2)
+      if (S.rows == 2) return go(backward_kernel<T, I::vpt, I::threads, 2, JOIN, DROP>);
+    return go(backward_kernel<T, I::vpt, I::threads, 1, JOIN, DROP>);
+  });
   if (st != MOE_OK || blocks == 1) return st;
   return launch_k(column_sum_kernel, dim3(ceil_div(kinds * c.H, 32)), dim3(1024), 0, s,
                   (const float*)a.ws, blocks, kinds, c.H, outs);
@@ -334,7 +390,7 @@ static moe_status_t backward(const moe_layer_t& c, const LayerArgs& a, cudaStrea
 using namespace lnorm;
 
 size_t layer_ws_bytes(const moe_layer_t& c) {
-  return (size_t)rows::max_blocks(shape_of(c)) * 2 * c.H * sizeof(float);
+  return (size_t)rows::max_blocks(shape_of(c, wide(c), rows_of(c))) * 2 * c.H * sizeof(float);
 }
 
 moe_status_t launch_layer_norm(const moe_layer_t& c, const LayerArgs& a, cudaStream_t s) {
@@ -365,7 +421,7 @@ __global__ void __launch_bounds__(256) dropout_kernel(const uint8_t* x, void* ou
 #pragma unroll
   for (int i = 0; i < kAhead; ++i)
     if (first + i * 256 < pieces) q[i].load(x + (first + i * 256) * Chunk<T>::kBytes);
-  const Philox rng = DROP ? Philox(D) : Philox();
+  Philox rng = DROP ? Philox(D) : Philox();
 #pragma unroll
   for (int i = 0; i < kAhead; ++i) {
     const int64_t at = first + i * 256;

@@ -103,9 +103,10 @@ __device__ __forceinline__ void load_w(const float* p, int i, F2 (&f)[4]) {
 }
 
 // How rows are spread: `group` threads (a multiple of 32) a row, chunk c of the row held by
-// thread c % group; a CTA works on `per` consecutive rows at once (a unit).
+// thread c % group; a group takes `rows` consecutive rows at once and a CTA `per` groups' (a unit).
 struct Shape {
   int T, H, chunks, group, per, units;
+  int rows = 1;
   float scale, offset, eps, inv_h;
   int n_in;           // row tensors read
   int stages;
@@ -115,7 +116,7 @@ struct Shape {
 // Sums of N values over a row's group, in every thread of it. Every thread of the CTA calls it,
 // whether its row exists or not. Two buffers used in turn make one barrier a reduction enough.
 struct Reducer {
-  float buf[2][3][kMaxThreads / 32];
+  float buf[2][4][kMaxThreads / 32];
 };
 template <int N, int M>
 __device__ __forceinline__ void group_sum(float (&v)[M], int group, Reducer& red, int& turn) {
@@ -141,7 +142,7 @@ __device__ __forceinline__ void group_sum(float (&v)[M], int group, Reducer& red
 template <typename T, int VPT>
 constexpr bool kRinged = VPT * (int)sizeof(T) <= 8;
 
-template <typename T, int VPT, int MAXIN>
+template <typename T, int VPT, int MAXIN, int ROWS = 1>
 struct Ring {
   static constexpr bool on = kRinged<T, VPT>;
   const Shape& S;
@@ -154,37 +155,40 @@ struct Ring {
   __device__ __forceinline__ Ring(const Shape& S_, uint8_t* smem, int local_, int g)
       : S(S_), local(local_) {
     row_bytes = (uint32_t)S.H * sizeof(T);
-    tensor_bytes = row_bytes * S.per;
+    tensor_bytes = row_bytes * S.per * ROWS;
     stage_bytes = tensor_bytes * S.n_in;
     step = S.group * Chunk<T>::kBytes;
     off = g * Chunk<T>::kBytes;
-    mine = smem + local * row_bytes + off;
+    mine = smem + local * ROWS * row_bytes + off;
     first = su32(mine);
 #pragma unroll
     for (int v = 0; v < VPT; ++v) has[v] = g + v * S.group < S.chunks;
   }
   __device__ __forceinline__ void issue(int u, int s) {  // one group of copies: unit u into stage s
-    if (!on) return;
-    const int t = u * S.per + local;
-    if (u < S.units && t < S.T) {
-      const int64_t from = (int64_t)t * row_bytes + off;
-      uint32_t dst = first + s * stage_bytes;
+    if constexpr (on) {
 #pragma unroll
-      for (int i = 0; i < MAXIN; ++i) {
-        if (i >= S.n_in) break;
-        const uint8_t* src = (const uint8_t*)S.in[i] + from;
+      for (int r = 0; r < ROWS; ++r) {
+        const int t = (u * S.per + local) * ROWS + r;
+        if (u >= S.units || t >= S.T) break;
+        const int64_t from = (int64_t)t * row_bytes + off;
+        uint32_t dst = first + s * stage_bytes + r * row_bytes;
 #pragma unroll
-        for (int v = 0; v < VPT; ++v) {
-          if (has[v]) {
+        for (int i = 0; i < MAXIN; ++i) {
+          if (i >= S.n_in) break;
+          const uint8_t* src = (const uint8_t*)S.in[i] + from;
 #pragma unroll
-            for (int b = 0; b < Chunk<T>::kBytes; b += 16)
-              cp_async16(dst + v * step + b, src + v * step + b, 16);
+          for (int v = 0; v < VPT; ++v) {
+            if (has[v]) {
+#pragma unroll
+              for (int b = 0; b < Chunk<T>::kBytes; b += 16)
+                cp_async16(dst + v * step + b, src + v * step + b, 16);
+            }
           }
+          dst += tensor_bytes;
         }
-        dst += tensor_bytes;
       }
+      cp_async_commit();
     }
-    cp_async_commit();
   }
   __device__ __forceinline__ void start() {  // the first units of this CTA
     for (int s = 0; s < S.stages; ++s) issue(blockIdx.x + s * gridDim.x, s);
@@ -195,9 +199,9 @@ struct Ring {
     else if (S.stages == 2) cp_async_wait<1>();
     else cp_async_wait<2>();
   }
-  // chunk v of tensor i in the current unit; t: its row
-  __device__ __forceinline__ void get(Chunk<T>& q, int i, int v, int t) const {
-    if (on) q.load_shared(mine + i * tensor_bytes + v * step);
+  // chunk v of tensor i in row r of the group's rows in the current unit; t: that row
+  __device__ __forceinline__ void get(Chunk<T>& q, int i, int v, int t, int r = 0) const {
+    if (on) q.load_shared(mine + i * tensor_bytes + r * row_bytes + v * step);
     else q.load((const uint8_t*)S.in[i] + (int64_t)t * row_bytes + off + v * step);
   }
   // the current stage's values have been used: its next unit
@@ -277,17 +281,18 @@ inline int max_blocks(const Shape& s) { return std::min(s.units, num_sms() * kMa
 
 // Fills in the ring's stages, as many as the budget of an SM's resident CTAs allows. Returns the
 // CTA's dynamic shared memory.
-inline size_t plan_ring(Shape& s, size_t es, int ctas, bool ringed) {
-  const size_t stage = (size_t)s.per * s.H * es * s.n_in;
+inline size_t plan_ring(Shape& s, size_t es, int ctas, bool ringed, size_t budget) {
+  const size_t stage = (size_t)s.per * s.rows * s.H * es * s.n_in;
   s.stages = 1;
   if (!ringed) return 0;
-  s.stages = (int)std::min<size_t>(kMaxStages, std::max<size_t>(1, kRingBudget / ctas / stage));
+  s.stages = (int)std::min<size_t>(kMaxStages, std::max<size_t>(1, budget / ctas / stage));
   return stage * s.stages;
 }
 
 template <typename... KArgs, typename... Args>
-inline moe_status_t run(void (*kern)(KArgs...), Shape& S, size_t es, size_t least, bool ringed,
-                        int max_ctas, int& blocks, cudaStream_t s, Args&&... args) {
+inline moe_status_t run_within(size_t budget, void (*kern)(KArgs...), Shape& S, size_t es,
+                               size_t least, bool ringed, int max_ctas, int& blocks, cudaStream_t s,
+                               Args&&... args) {
   const int threads = S.group * S.per;
   // CTAs an SM: what their registers allow (asked once a kernel, size and device), shared memory
   // being divided among them
@@ -314,11 +319,18 @@ inline moe_status_t run(void (*kern)(KArgs...), Shape& S, size_t es, size_t leas
     *hit = {(void*)kern, dev, threads, n};
   }
   int ctas = std::min(hit->ctas, max_ctas);
-  size_t smem = std::max(plan_ring(S, es, ctas, ringed), least);
+  size_t smem = std::max(plan_ring(S, es, ctas, ringed, budget), least);
   ctas = std::max(1, std::min<int>(ctas, (int)(220 * 1024 / (smem + 1024))));
   blocks = std::min(S.units, num_sms() * ctas);
   return launch_k(kern, dim3(blocks), dim3(threads), smem, s, (const Shape&)S,
                   std::forward<Args>(args)...);
+}
+
+template <typename... KArgs, typename... Args>
+inline moe_status_t run(void (*kern)(KArgs...), Shape& S, size_t es, size_t least, bool ringed,
+                        int max_ctas, int& blocks, cudaStream_t s, Args&&... args) {
+  return run_within(kRingBudget, kern, S, es, least, ringed, max_ctas, blocks, s,
+                    std::forward<Args>(args)...);
 }
 
 }  // namespace rows
