@@ -5,12 +5,12 @@
 // Both move rows and do next to no arithmetic: HBM bounds them. The gradient's sum has to be the same
 // every run, and a token's rows lie anywhere, so the tokens are sorted first (stably, by id) and runs
 // of one id summed in that order, in fp32:
-//   sort_fill  one cluster of 8 CTAs sorts (id, t) by radix passes of up to 9 bits; the other CTAs write
-//              the zeros of ids that do not occur meanwhile, which is most of what a dense gradient writes
-//   run_sum    a warp sums 32 sorted rows in a slice of 32 pieces of 16 bytes, and writes every run that
+//   sort_fill  one CTA, or a cluster of 8, sorts (id, t) by radix passes of up to 9 bits; the other CTAs
+//              write the zeros of ids that do not occur meanwhile, most of what a dense gradient writes
+//   run_sum    a warp sums 16 sorted rows in a slice of 32 pieces of 16 bytes, and writes every run that
 //              lies inside; a run that crosses to other warps' rows leaves fp32 partial sums
 //   join       the partial sums of a run are added in order: a run of any length is spread over as many
-//              warps as it has rows / 32
+//              warps as it has rows / 16
 #include "stack.cuh"
 #include "tc_ptx.cuh"
 #include "train.cuh"
@@ -62,41 +62,172 @@ __global__ void __launch_bounds__(256) embed_kernel(const void* __restrict__ tok
 }
 
 // ------------------------------------------------------------------- sorting, and zeros
-constexpr int kSorters = 8;      // CTAs of the sorting cluster
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kHeld = 8;         // keys that a thread holds in registers
+constexpr int kHeldCta = kSortThreads * kHeld;
+constexpr int kCluster = 8;      // CTAs that sort together
+constexpr int kAloneUpTo = 2048; // tokens that one CTA sorts by itself
 constexpr int kDigit = 9;        // bits of a pass at most
 constexpr int kBins = 1 << kDigit;
-constexpr int kFillRows = 1 << 16;  // rows whose marks fit the fill CTAs' shared memory
+constexpr int kFillRows = 1 << 16;   // rows whose marks fit the fill CTAs' shared memory
+constexpr int kZeroBytes = 1 << 14;  // zeros that one bulk copy writes at most
 
 struct SortArgs {
   const void* tokens;
   int T, V;
   int passes, bits;  // of a pass
-  uint32_t *key[2];
-  int32_t *at[2];    // pass p writes key[p & 1], at[p & 1]
-  uint4* table;      // rows to zero, or NULL
-  int vec;           // 16-byte pieces of a row
+  uint32_t* key[2];  // the last pass writes key[0] and at[0]
+  int32_t* at[2];
+  uint8_t* table;    // rows to zero, or NULL
+  int64_t row_bytes;
 };
 
 struct SortShared {
   uint32_t hist[kSortWarps][kBins];
   uint32_t total[kBins], base[kBins], scan[kBins / 32];
+  uint64_t held[kHeldCta];  // key and token, where a pass of the held sort puts them
+};
+struct FillShared {
+  uint4 zeros[kZeroBytes / 16];
+  uint8_t seen[kFillRows];
 };
 
+__device__ __forceinline__ uint32_t ld_cluster(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_cluster(uint32_t addr, uint64_t v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
+}
+
+// After the warps have counted their digits in hist: exclusive sums over the CTA's warps into hist, and
+// over lower digits and the cluster's lower CTAs into base. A key's place is then base + hist + its
+// rank among its warp's keys of the digit. Called by all threads, which may then read both.
+template <int CL>
+__device__ __forceinline__ void digit_places(SortShared& sh, int bins) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, d = threadIdx.x;
+  const int rank = CL > 1 ? cluster_ctarank() : 0;
+  __syncthreads();
+  uint32_t mine = 0;
+  if (d < bins) {
+#pragma unroll
+    for (int w = 0; w < kSortWarps; ++w) {
+      const uint32_t c = sh.hist[w][d];
+      sh.hist[w][d] = mine;
+      mine += c;
+    }
+    sh.total[d] = mine;
+  }
+  uint32_t all = mine, lower = 0;
+  if (CL > 1) {
+    cluster_sync();
+    if (d < bins) {
+      all = 0;
+#pragma unroll
+      for (int c = 0; c < CL; ++c) {
+        const uint32_t v = ld_cluster(cluster_addr(&sh.total[d], c));
+        if (c < rank) lower += v;
+        all += v;
+      }
+    }
+  }
+  uint32_t inc = all;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const uint32_t o = __shfl_up_sync(0xffffffffu, inc, off);
+    if (lane >= off) inc += o;
+  }
+  if (d < kBins && lane == 31) sh.scan[warp] = inc;
+  __syncthreads();
+  if (d < bins) {
+    uint32_t before = 0;
+    for (int w = 0; w < warp; ++w) before += sh.scan[w];
+    sh.base[d] = before + inc - all + lower;
+  }
+  __syncthreads();
+}
+
+// Up to kHeld keys a thread, in registers through all passes: a pass ranks them as it counts them and puts
+// them into shared memory (of the CTA that holds the place) for the next.
+template <bool WIDE, int CL>
+__device__ __forceinline__ void sort_held(const SortArgs& A, SortShared& sh) {
+  const int rank = CL > 1 ? cluster_ctarank() : 0, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t below = (1u << lane) - 1;
+  const int each = (A.T + CL * kSortThreads - 1) / (CL * kSortThreads);  // keys of a thread
+  const int first = ((rank * kSortWarps + warp) * each) * 32 + lane;     // and its first, 32 apart
+  const int cta_first = rank * kSortThreads * each;
+  const int bins = 1 << A.bits;
+  uint32_t key[kHeld], place[kHeld];
+  int32_t at[kHeld];
+#pragma unroll
+  for (int j = 0; j < kHeld; ++j) {
+    at[j] = first + j * 32;
+    key[j] = j < each && at[j] < A.T ? (uint32_t)id_of<WIDE>(A.tokens, at[j], A.V) : 0;
+  }
+  for (int pass = 0; pass < A.passes; ++pass) {
+    const int shift = pass * A.bits;
+    uint32_t* hist = sh.hist[warp];
+    for (int d = lane; d < bins; d += 32) hist[d] = 0;
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < kHeld; ++j) {
+      if (j >= each) break;
+      const bool live = first + j * 32 < A.T;
+      const uint32_t d = live ? key[j] >> shift & (bins - 1) : kBins;
+      const uint32_t same = __match_any_sync(0xffffffffu, d);
+      if (live) place[j] = hist[d] + __popc(same & below);
+      __syncwarp();
+      if (live && !(same & below)) hist[d] += __popc(same);
+      __syncwarp();
+    }
+    digit_places<CL>(sh, bins);
+    const bool last = pass == A.passes - 1;
+#pragma unroll
+    for (int j = 0; j < kHeld; ++j) {
+      if (j >= each || first + j * 32 >= A.T) break;
+      const uint32_t d = key[j] >> shift & (bins - 1);
+      const uint32_t to = place[j] + hist[d] + sh.base[d];
+      const uint64_t held = (uint64_t)key[j] << 32 | (uint32_t)at[j];
+      if (last) {
+        A.key[0][to] = key[j];
+        A.at[0][to] = at[j];
+      } else if (CL == 1) {
+        sh.held[to] = held;
+      } else {
+        const uint32_t span = kSortThreads * each, cta = to / span;
+        st_cluster(cluster_addr(&sh.held[to - cta * span], cta), held);
+      }
+    }
+    if (CL > 1) cluster_sync();  // after the last pass too: no CTA leaves while its totals are read
+    else __syncthreads();
+    if (last) break;
+#pragma unroll
+    for (int j = 0; j < kHeld; ++j) {
+      if (j >= each) break;
+      const uint64_t held = sh.held[first - cta_first + j * 32];
+      key[j] = (uint32_t)(held >> 32);
+      at[j] = (int32_t)held;
+    }
+    __syncthreads();
+  }
+}
+
+// Any number of keys: read from global memory twice a pass, to count and to place them.
 template <bool WIDE>
-__device__ __forceinline__ void sort_tokens(const SortArgs& A, SortShared& sh) {
+__device__ __forceinline__ void sort_any(const SortArgs& A, SortShared& sh) {
   const int rank = cluster_ctarank(), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t below = (1u << lane) - 1;
   // every warp of the cluster takes a run of tokens, in order of CTA and warp
-  const int64_t each = ceil_div64(ceil_div64(A.T, kSorters * kSortWarps), 32) * 32;
+  const int64_t each = ceil_div64(ceil_div64(A.T, kCluster * kSortWarps), 32) * 32;
   const int64_t first = min((rank * kSortWarps + warp) * each, (int64_t)A.T);
   const int64_t end = min(first + each, (int64_t)A.T);
   const int bins = 1 << A.bits;
   for (int pass = 0; pass < A.passes; ++pass) {
-    const int shift = pass * A.bits;
-    const uint32_t* from = A.key[(pass & 1) ^ 1];
-    const int32_t* from_at = A.at[(pass & 1) ^ 1];
+    const int shift = pass * A.bits, dst = (A.passes - 1 - pass) & 1;
+    const uint32_t* from = A.key[dst ^ 1];
+    const int32_t* from_at = A.at[dst ^ 1];
     auto key_of = [&](int64_t i) {
       return pass == 0 ? (uint32_t)id_of<WIDE>(A.tokens, i, A.V) : __ldcg(from + i);
     };
@@ -110,46 +241,7 @@ __device__ __forceinline__ void sort_tokens(const SortArgs& A, SortShared& sh) {
       if (live && !(same & below)) hist[d] += __popc(same);
       __syncwarp();
     }
-    __syncthreads();
-    // counts of a digit: exclusive sums over the CTA's warps, then over the cluster and the digits
-    for (int d = threadIdx.x; d < bins; d += kSortThreads) {
-      uint32_t sum = 0;
-#pragma unroll 8
-      for (int w = 0; w < kSortWarps; ++w) {
-        const uint32_t c = sh.hist[w][d];
-        sh.hist[w][d] = sum;
-        sum += c;
-      }
-      sh.total[d] = sum;
-    }
-    cluster_sync();
-    uint32_t all = 0, lower = 0;
-    const int d = threadIdx.x;
-    if (d < bins) {
-#pragma unroll
-      for (int c = 0; c < kSorters; ++c) {
-        uint32_t v;
-        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr(&sh.total[d], c)) : "memory");
-        if (c < rank) lower += v;
-        all += v;
-      }
-    }
-    uint32_t inc = all;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const uint32_t o = __shfl_up_sync(0xffffffffu, inc, off);
-      if (lane >= off) inc += o;
-    }
-    if (d < kBins && lane == 31) sh.scan[warp] = inc;
-    __syncthreads();
-    if (d < bins) {
-      uint32_t before = 0;
-      for (int w = 0; w < warp; ++w) before += sh.scan[w];
-      sh.base[d] = before + inc - all + lower;
-    }
-    __syncthreads();
-    uint32_t* to = A.key[pass & 1];
-    int32_t* to_at = A.at[pass & 1];
+    digit_places<kCluster>(sh, bins);
     for (int64_t i0 = first; i0 < end; i0 += 32) {
       const int64_t i = i0 + lane;
       const bool live = i < end;
@@ -163,8 +255,8 @@ __device__ __forceinline__ void sort_tokens(const SortArgs& A, SortShared& sh) {
       if (live && !(same & below)) hist[d] += __popc(same);
       __syncwarp();
       if (live) {
-        __stcg(to + place, k);
-        __stcg(to_at + place, at);
+        __stcg(A.key[dst] + place, k);
+        __stcg(A.at[dst] + place, at);
       }
     }
     __threadfence();
@@ -172,41 +264,97 @@ __device__ __forceinline__ void sort_tokens(const SortArgs& A, SortShared& sh) {
   }
 }
 
-// Zeros into the rows of ids that do not occur: the CTA marks the ids of its rows that do.
+// Zeros into the rows of ids that do not occur: the CTA marks the ids of its rows that do, and every
+// thread has the others' rows written by bulk copies from a buffer of zeros (7 TB/s; with a warp's
+// stores row by row 4.1).
 template <bool WIDE>
-__device__ __forceinline__ void fill_zeros(const SortArgs& A, uint8_t* seen, int cta, int ctas) {
+__device__ __forceinline__ void fill_zeros(const SortArgs& A, FillShared& sh, int cta, int ctas) {
   const int64_t r0 = (int64_t)A.V * cta / ctas, r1 = (int64_t)A.V * (cta + 1) / ctas;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int i = threadIdx.x; i < kZeroBytes / 16; i += kSortThreads) sh.zeros[i] = make_uint4(0, 0, 0, 0);
+  fence_proxy_async_smem();
+  const uint32_t zeros = su32(sh.zeros);
   for (int64_t s0 = r0; s0 < r1; s0 += kFillRows) {
     const int rows = (int)min((int64_t)kFillRows, r1 - s0);
-    for (int i = threadIdx.x; i < rows; i += kSortThreads) seen[i] = 0;
+    for (int i = threadIdx.x; i < rows; i += kSortThreads) sh.seen[i] = 0;
     __syncthreads();
+#pragma unroll 4
     for (int64_t t = threadIdx.x; t < A.T; t += kSortThreads) {
       const int64_t i = id_of<WIDE>(A.tokens, t, A.V) - s0;
-      if (i >= 0 && i < rows) seen[i] = 1;
+      if (i >= 0 && i < rows) sh.seen[i] = 1;
     }
     __syncthreads();
-    for (int i = warp; i < rows; i += kSortWarps) {
-      if (seen[i]) continue;
-      uint4* row = A.table + (s0 + i) * A.vec;
-      for (int v = lane; v < A.vec; v += 32) __stcs(row + v, make_uint4(0, 0, 0, 0));
+    for (int i = threadIdx.x; i < rows; i += kSortThreads) {
+      if (sh.seen[i]) continue;
+      uint8_t* row = A.table + (s0 + i) * A.row_bytes;
+      for (int64_t b = 0; b < A.row_bytes; b += kZeroBytes) {
+        const uint32_t n = (uint32_t)min((int64_t)kZeroBytes, A.row_bytes - b);
+        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(row + b), "r"(zeros), "r"(n)
+                     : "memory");
+      }
     }
     __syncthreads();
   }
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
-template <bool WIDE>
-__global__ void __cluster_dims__(kSorters, 1, 1) __launch_bounds__(kSortThreads, 1)
-    sort_fill_kernel(const __grid_constant__ SortArgs A) {
-  extern __shared__ __align__(16) uint8_t smem[];
+// CL: CTAs of the cluster that sorts, the grid's first. HELD: at most CL * kHeldCta tokens.
+template <bool WIDE, int CL, bool HELD>
+__global__ void __launch_bounds__(kSortThreads, 1) sort_fill_kernel(const __grid_constant__ SortArgs A) {
+  extern __shared__ __align__(128) uint8_t smem[];
   pdl_wait();
   pdl_trigger();
-  if (blockIdx.x < kSorters) sort_tokens<WIDE>(A, *(SortShared*)smem);
-  else fill_zeros<WIDE>(A, smem, blockIdx.x - kSorters, gridDim.x - kSorters);
+  if (blockIdx.x >= CL) fill_zeros<WIDE>(A, *(FillShared*)smem, blockIdx.x - CL, gridDim.x - CL);
+  else if constexpr (HELD) sort_held<WIDE, CL>(A, *(SortShared*)smem);
+  else sort_any<WIDE>(A, *(SortShared*)smem);
+}
+
+template <bool WIDE, int CL, bool HELD>
+static moe_status_t sort_fill(const SortArgs& A, cudaStream_t s) {
+  auto kern = sort_fill_kernel<WIDE, CL, HELD>;
+  const size_t smem = std::max(sizeof(SortShared), sizeof(FillShared));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(CL);
+  cfg.blockDim = dim3(kSortThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = CL;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  // clusters that the device holds at once (asked once a kernel and device): the SMs of a group are no
+  // multiple of 8, and with a cluster more than fits the zeros took a second round
+  static thread_local int known_dev = -1, clusters = 0;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev != known_dev) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+      return MOE_ERR_CUDA;
+    clusters = num_sms();
+    if (CL > 1 && cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg) != cudaSuccess) return MOE_ERR_CUDA;
+    known_dev = dev;
+  }
+  if (A.table) cfg.gridDim = dim3(std::max(2, clusters) * CL);  // the first one sorts, the others fill
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, A) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+template <bool WIDE>
+static moe_status_t sort_fill(const SortArgs& A, cudaStream_t s) {
+  // one CTA where that is as quick, or hidden behind the zeros (20 us for 8192 tokens, 140 MB of zeros): then
+  // all other SMs write, not only those of whole clusters
+  const bool hidden = A.T <= kHeldCta && A.table && A.V * A.row_bytes >= (int64_t)A.T * 16384;
+  if (A.T <= kAloneUpTo || hidden) return sort_fill<WIDE, 1, true>(A, s);
+  if (A.T <= kCluster * kHeldCta) return sort_fill<WIDE, kCluster, true>(A, s);
+  return sort_fill<WIDE, kCluster, false>(A, s);
 }
 
 // ------------------------------------------------------------------- sums of runs
-constexpr int kRun = 32;  // sorted rows of a warp: a lane keeps the id and the token of one
+constexpr int kRun = 16;  // sorted rows of a warp: a lane keeps the id and the token of one
 
 template <typename T, typename O>
 struct RowPiece {  // the values of one 16-byte piece of T
@@ -448,19 +596,12 @@ moe_status_t launch_embed_backward(const void* dx, const void* tokens, bool wide
     A.key[i] = (uint32_t*)(w + l.key[i]);
     A.at[i] = (int32_t*)(w + l.at[i]);
   }
-  A.table = accumulate ? nullptr : (uint4*)dtable;
-  A.vec = (int)((size_t)H * dtype_size(out_dt) / 16);
-  auto sort = [&](auto kern) {
-    const size_t smem = std::max(sizeof(SortShared), (size_t)kFillRows);
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-      return MOE_ERR_CUDA;
-    const int fill = accumulate ? 0 : std::max(1, num_sms() / kSorters - 1) * kSorters;
-    return launch_k(kern, dim3(kSorters + fill), dim3(kSortThreads), smem, s, (const SortArgs&)A);
-  };
-  moe_status_t st = wide ? sort(sort_fill_kernel<true>) : sort(sort_fill_kernel<false>);
+  A.table = accumulate ? nullptr : (uint8_t*)dtable;
+  A.row_bytes = (int64_t)H * dtype_size(out_dt);
+  moe_status_t st = wide ? sort_fill<true>(A, s) : sort_fill<false>(A, s);
   if (st != MOE_OK) return st;
-  const uint32_t* keys = A.key[(A.passes - 1) & 1];
-  const int32_t* at = A.at[(A.passes - 1) & 1];
+  const uint32_t* keys = A.key[0];
+  const int32_t* at = A.at[0];
   float* part = (float*)(w + l.part);
   const int vec = (int)((size_t)H * dtype_size(dt) / 16), slices = ceil_div(vec, 32);
   const int chunks = ceil_div(T, kRun);

@@ -230,17 +230,26 @@ __device__ __forceinline__ void leave_columns(const Shape& S, uint8_t* smem, int
                                               float factor, float* ws, const Outs& outs) {
   float* to = gridDim.x == 1 ? outs.p[kind] : ws + ((int64_t)blockIdx.x * kinds + kind) * S.H;
   float* all = S.per > 1 ? (float*)smem + (int64_t)local * S.H : to;
+  const bool pieces = ((uintptr_t)all & 15) == 0;  // a result need not start on 16 bytes
   if (S.per > 1) __syncthreads();
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
     const int c = g + v * S.group;
     if (c >= S.chunks) continue;
+    float f[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      float lo, hi;
-      split(s[v][i], lo, hi);
-      all[c * 8 + 2 * i] = lo * factor;
-      all[c * 8 + 2 * i + 1] = hi * factor;
+      split(s[v][i], f[2 * i], f[2 * i + 1]);
+      f[2 * i] *= factor;
+      f[2 * i + 1] *= factor;
+    }
+    if (pieces) {
+      float4* at = (float4*)(all + c * 8);
+      at[0] = make_float4(f[0], f[1], f[2], f[3]);
+      at[1] = make_float4(f[4], f[5], f[6], f[7]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) all[c * 8 + i] = f[i];
     }
   }
   if (S.per == 1) return;
