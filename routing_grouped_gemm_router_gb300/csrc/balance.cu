@@ -100,6 +100,17 @@ __device__ __forceinline__ void load_lane(const float* row, bool in, int E, int 
   }
 }
 
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float reciprocal_fast(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 // A token's probabilities from its logits, in the lanes of its group.
 template <int N, bool SIGMOID>
 struct Token {
@@ -113,16 +124,19 @@ struct Token {
 #pragma unroll
     for (int i = 0; i < N; ++i) m = fmaxf(m, z[i]);
     m = group_max(m, group);
+    // exponentials of base 2: off by 2 steps, and half a step for every unit of the arguments' size
+    constexpr float kLog2e = 1.4426950408889634f;
+    const float shift = -m * kLog2e;
     float sum = 0.f, total = 0.f;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      p[i] = expf(z[i] - m);
+      p[i] = exp2_fast(fmaf(z[i], kLog2e, shift));
       sum += p[i];
     }
     if constexpr (SIGMOID) {
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const float x = expf(-fabsf(z[i])), d = __fdividef(1.f, 1.f + x);
+        const float x = exp2_fast(-fabsf(z[i]) * kLog2e), d = reciprocal_fast(1.f + x);
         soft[i] = p[i];
         p[i] = m < 0.f ? p[i] * d : z[i] >= 0.f ? d : x * d;
         slope[i] = z[i] >= 0.f ? x * d : d;
@@ -141,112 +155,144 @@ struct Token {
   }
 };
 
-// Sums over the chunks' tokens.
+// The tokens of a tile, one a group, and whether they take part; asked for a tile ahead.
+template <int N, bool VEC>
+struct Tile {
+  float z[N];
+  bool live;
+  __device__ __forceinline__ void ask(const Args& A, int64_t t, int64_t end, int gl) {
+    live = t < end;
+    load_lane<N, VEC>(A.logits + t * A.E, live, A.E, gl, A.group, -INFINITY, z);
+    if (live && A.mask) live = A.mask[t];
+  }
+  __device__ __forceinline__ void add_bias(const Args& A, int gl) {
+    if (!A.bias) return;
+    float bias[N];
+    load_lane<N, VEC>(A.bias, true, A.E, gl, A.group, 0.f, bias);
+#pragma unroll
+    for (int i = 0; i < N; ++i) z[i] += bias[i];
+  }
+};
+
+// Sums over the chunks' tokens. All that a chunk's first tile needs is asked for before anything is waited
+// for; a tile's probabilities are computed once, and added to every sequence that it meets.
 template <int N, bool VEC, bool SIGMOID>
 __global__ void __launch_bounds__(kThreads, 2) partial_kernel(const __grid_constant__ Args A,
-                                                           int* arrived) {
-  constexpr int HALF = kWarps / 2;
-  __shared__ __align__(16) float sums[HALF * 512];  // [warps / 2][E]
+                                                              int* arrived) {
+  __shared__ __align__(16) float sums[kThreads * N];  // [groups][lanes * N]: every token group's sums
+  __shared__ float part[kThreads];                    // [parts][lanes * N]: N groups' each
   __shared__ int cnt[512];
-  __shared__ float zs[kWarps];
-  __shared__ int ns[kWarps];
+  __shared__ float zs[kThreads];  // of the groups
+  __shared__ int ns[kThreads];
   __shared__ Offsets off;
   pdl_wait();
   pdl_trigger();
-  if (blockIdx.x == 0 && threadIdx.x == 0) *arrived = 0;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int G = A.group, gl = lane & (G - 1), groups = kThreads / G, sub = threadIdx.x / G;
   const int t0 = blockIdx.x * A.per_chunk, t1 = min(A.T, t0 + A.per_chunk);
+  Tile<N, VEC> tile;
+  tile.ask(A, (int64_t)t0 + sub, t1, gl);
+  // one slot of the chunk a thread; the few beyond are read when they are counted
+  const int slots = (t1 - t0) * A.slots;
+  auto id_of = [&](int i, int t) {  // slot i of the chunk, of token t; -1: not counted
+    if (i >= slots || i - (t - t0) * A.slots >= A.k) return -1;
+    const int id = __ldg(A.ids + (int64_t)t0 * A.slots + i);
+    return (!A.mask || A.mask[t]) && id < A.E ? id : -1;
+  };
+  const int my_token = t0 + (int)(threadIdx.x / (unsigned)A.slots), my_id = id_of(threadIdx.x, my_token);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *arrived = 0;
   off.fetch(A);
-  for (int t = t0; t < t1;) {
-    const Run r = off.run(A, t, t1);
-    if (r.s < 0) {
-      t = r.end;
-      continue;
-    }
+  int start = t0;
+  Run r = off.run(A, t0, t1);
+  float acc[N], z2 = 0.f;
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) acc[i] = 0.f;
+
+  auto flush = [&]() {  // the sums of run r, which began at `start`, into its slot
     for (int e = threadIdx.x; e < A.E; e += kThreads) cnt[e] = 0;
+    // all groups' sums through shared memory, first over N groups, then over those, in order
+    const int width = G * N;
+    float* row = sums + sub * width;
+    if constexpr (VEC) {
+#pragma unroll
+      for (int i = 0; i < N; i += 4)
+        *(float4*)(row + expert<N, VEC>(i, gl, G)) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) row[expert<N, VEC>(i, gl, G)] = acc[i];
+    }
+    if (gl == 0) zs[sub] = z2;
+    if (gl == 0) ns[sub] = n;
     __syncthreads();
-    const int slots = (r.end - t) * A.slots;
-    for (int i = threadIdx.x; i < slots; i += kThreads) {
-      const int id = __ldg(A.ids + (int64_t)t * A.slots + i), j = i % A.slots;
-      const bool live = !A.mask || A.mask[t + i / A.slots];
-      if (live && j < A.k && id >= 0 && id < A.E) atomicAdd(&cnt[id], 1);
+    const int column = threadIdx.x % width, first = threadIdx.x / width * N;
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) s += sums[(first + i) * width + column];
+    part[threadIdx.x] = s;
+    if (my_id >= 0 && my_token >= start && my_token < r.end) atomicAdd(&cnt[my_id], 1);
+    for (int i = threadIdx.x + kThreads; i < slots; i += kThreads) {
+      const int t = t0 + i / A.slots;
+      if (t < start || t >= r.end) continue;
+      const int id = id_of(i, t);
+      if (id >= 0) atomicAdd(&cnt[id], 1);
     }
-    float acc[N], z2 = 0.f;
-    int n = 0;
-#pragma unroll
-    for (int i = 0; i < N; ++i) acc[i] = 0.f;
-    for (int b = t; b < r.end; b += groups) {
-      const int64_t mine = (int64_t)b + sub;
-      const bool in = mine < r.end;
-      float z[N];
-      load_lane<N, VEC>(A.logits + mine * A.E, in, A.E, gl, G, -INFINITY, z);
-      const bool live = in && (!A.mask || A.mask[mine]);
-      if (A.bias) {
-        float bias[N];
-        load_lane<N, VEC>(A.bias, true, A.E, gl, G, 0.f, bias);
-#pragma unroll
-        for (int i = 0; i < N; ++i) z[i] += bias[i];
-      }
-      Token<N, SIGMOID> k;
-      k.set(z, G);
-      if (live) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) acc[i] += k.p[i];
-        z2 += k.lse * k.lse;
-        ++n;
-      }
-    }
-    // over a warp's tokens, then over the warps, in a fixed order
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      for (int o = G; o < 32; o <<= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
-    for (int o = G; o < 32; o <<= 1) {
-      z2 += __shfl_xor_sync(0xffffffffu, z2, o);
-      n += __shfl_xor_sync(0xffffffffu, n, o);
-    }
-    if (lane == 0) {
-      zs[warp] = z2;
-      ns[warp] = n;
-    }
-    float* row = sums + (warp % HALF) * A.E;
-    auto store = [&](bool add) {
-      if (lane >= G) return;
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const int e = expert<N, VEC>(i, gl, G);
-        if (e < A.E) row[e] = add ? row[e] + acc[i] : acc[i];
-      }
-    };
-    if (warp >= HALF) store(false);
-    __syncthreads();
-    if (warp < HALF) store(true);
     __syncthreads();
     const int64_t slot = (int64_t)blockIdx.x + r.s;
     for (int e = threadIdx.x; e < A.E; e += kThreads) {
-      float s = 0.f;
-#pragma unroll
-      for (int w = 0; w < HALF; ++w) s += sums[w * A.E + e];
+      s = 0.f;
+      for (int w = e; w < kThreads; w += width) s += part[w];
       A.part_p[slot * A.E + e] = s;
       A.part_c[slot * A.E + e] = cnt[e];
     }
     if (warp == kWarps - 1) {
-      const float s = warp_total(lane < kWarps ? zs[lane] : 0.f);
-      const int c = __reduce_add_sync(0xffffffffu, lane < kWarps ? ns[lane] : 0);
+      s = 0.f;
+      int c = 0;
+      for (int i = lane; i < groups; i += 32) {
+        s += zs[i];
+        c += ns[i];
+      }
+      s = warp_total(s);
+      c = __reduce_add_sync(0xffffffffu, c);
       if (lane == 0) {
         A.part_z[slot] = s;
         A.part_n[slot] = c;
       }
     }
     __syncthreads();
-    t = r.end;
+#pragma unroll
+    for (int i = 0; i < N; ++i) acc[i] = 0.f;
+    z2 = 0.f;
+    n = 0;
+  };
+
+  for (int b = t0; b < t1; b += groups) {
+    const int mine = b + sub;
+    const bool live = tile.live;
+    tile.add_bias(A, gl);
+    Token<N, SIGMOID> k;
+    k.set(tile.z, G);
+    tile.ask(A, (int64_t)mine + groups, t1, gl);
+    for (;;) {
+      if (r.s >= 0 && live && mine >= start && mine < r.end) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) acc[i] += k.p[i];
+        z2 += k.lse * k.lse;
+        ++n;
+      }
+      if (r.end - groups > b) break;  // the run goes on behind the tile
+      if (r.s >= 0) flush();
+      if (r.end >= t1) break;
+      start = r.end;
+      r = off.run(A, start, t1);
+    }
   }
 }
 
 struct Sums {  // outputs, and what the sequences leave for the last CTA
   float *losses, *prob;
   int32_t *counts, *tokens, *totals;
-  float *loss_part, *z_part;  // [S][column blocks], [S]
+  float *loss_part, *z_part;  // [S][E / 8 rounded up], [S]
   int* arrived;
 };
 
@@ -278,20 +324,20 @@ struct BlockSum {
   }
 };
 
-// A CTA adds up 32 experts of a sequence; the one that ends last adds up the losses. WARPS: many for few
-// sequences, which have many slots.
+// A CTA adds up 8 experts of a sequence, its threads slots side by side; the one that ends last adds up
+// the losses. WARPS: many for few sequences, which have many slots.
 template <int WARPS>
 __global__ void __launch_bounds__(WARPS * 32) sequence_kernel(const __grid_constant__ Args A,
                                                               const __grid_constant__ Sums B) {
-  __shared__ float sp[WARPS][33];
-  __shared__ int sc[WARPS][33];
+  __shared__ float sp[WARPS][8];
+  __shared__ int sc[WARPS][8];
   __shared__ BlockSum<WARPS> all;
   __shared__ bool last;
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int blocks = (A.E + 31) / 32;
-  const int s = blockIdx.x / blocks, eb = blockIdx.x % blocks, e = eb * 32 + lane;
+  const int blocks = (A.E + 7) / 8;
+  const int s = blockIdx.x / blocks, eb = blockIdx.x % blocks, e = eb * 8 + (lane & 7);
   int a = A.offsets ? __ldg(A.offsets + s) : 0, b = A.offsets ? __ldg(A.offsets + s + 1) : A.T;
   if (a < 0 || b < a || b > A.T) {
     if (threadIdx.x == 0) atomicExch(&g_status, kStatusBadOffsets);
@@ -300,38 +346,51 @@ __global__ void __launch_bounds__(WARPS * 32) sequence_kernel(const __grid_const
   }
   const int64_t first = a / A.per_chunk + s;
   const int chunks = b > a ? (b - 1) / A.per_chunk - a / A.per_chunk + 1 : 0;
-  float p = 0.f, z = 0.f, none = 0.f;
-  int c = 0, n = 0, zero = 0;
-#pragma unroll 8
-  for (int i = warp; i < chunks; i += WARPS) {
+  // asked for first, added last: their way from L2 is the same as the others'
+  const bool some_here = (int)threadIdx.x < chunks;
+  const int n_first = some_here ? A.part_n[first + threadIdx.x] : 0;
+  const float z_first = some_here ? A.part_z[first + threadIdx.x] : 0.f;
+  float p = 0.f, none = 0.f;
+  int c = 0, zero = 0;
+#pragma unroll 5
+  for (int i = threadIdx.x >> 3; i < chunks; i += WARPS * 4) {
     const int64_t slot = first + i;
     if (e < A.E) {
       p += A.part_p[slot * A.E + e];
       c += A.part_c[slot * A.E + e];
     }
   }
-  for (int i = threadIdx.x; i < chunks; i += WARPS * 32) {
+  int n = n_first;
+  float z = z_first;
+  for (int i = threadIdx.x + WARPS * 32; i < chunks; i += WARPS * 32) {
     n += A.part_n[first + i];
     z += A.part_z[first + i];
   }
-  sp[warp][lane] = p;
-  sc[warp][lane] = c;
+#pragma unroll
+  for (int o = 8; o < 32; o <<= 1) {
+    p += __shfl_xor_sync(0xffffffffu, p, o);
+    c += __shfl_xor_sync(0xffffffffu, c, o);
+  }
+  if (lane < 8) {
+    sp[warp][lane] = p;
+    sc[warp][lane] = c;
+  }
   all.add(z, none, n, zero);
   if (warp == 0) {
     p = 0.f;
     c = 0;
 #pragma unroll
     for (int w = 0; w < WARPS; ++w) {
-      p += sp[w][lane];
-      c += sc[w][lane];
+      p += sp[w][lane & 7];
+      c += sc[w][lane & 7];
     }
     const float inv = n ? 1.f / (float)n : 0.f;
     p *= inv;
-    if (e < A.E) {
+    if (lane < 8 && e < A.E) {
       B.prob[(int64_t)s * A.E + e] = p;
       B.counts[(int64_t)s * A.E + e] = c;
     }
-    const float loss = warp_total(e < A.E ? (float)c * ((float)A.E / (float)A.k) * inv * p : 0.f);
+    const float loss = warp_total(lane < 8 && e < A.E ? (float)c * ((float)A.E / (float)A.k) * inv * p : 0.f);
     if (lane == 0) {
       B.loss_part[blockIdx.x] = loss;
       if (eb == 0) {
@@ -377,67 +436,73 @@ __global__ void __launch_bounds__(kBackThreads) backward_kernel(
   const int lane = threadIdx.x & 31;
   const int G = A.group, gl = lane & (G - 1), groups = kBackThreads / G, sub = threadIdx.x / G;
   const int t0 = blockIdx.x * A.per_chunk, t1 = min(A.T, t0 + A.per_chunk);
+  Tile<N, VEC> tile;
+  tile.ask(A, (int64_t)t0 + sub, t1, gl);
   const int some = __ldg(totals), all = __ldg(totals + 1);
   const float d0 = __ldg(dlosses), d1 = __ldg(dlosses + 1) * 2.f / (float)max(all, 1);
   off.fetch(A);
-  for (int t = t0; t < t1;) {
-    const Run r = off.run(A, t, t1);
-    float f = 0.f, g[N];
-    if (r.s >= 0) {
-      const float n = (float)max(__ldg(tokens + r.s), 1);
-      f = d0 * ((float)A.E / (float)A.k) / (n * n * (float)max(some, 1));
-    }
-    load_lane<N, VEC>((const float*)counts + (int64_t)max(r.s, 0) * A.E, r.s >= 0, A.E, gl, G, 0.f, g);
+  float g[N];
+  auto weights = [&](int s) {  // of sequence s: d balance / d p
+    if (s < 0) return;
+    const float n = (float)max(__ldg(tokens + s), 1);
+    const float f = d0 * ((float)A.E / (float)A.k) / (n * n * (float)max(some, 1));
+    load_lane<N, VEC>((const float*)counts + (int64_t)s * A.E, true, A.E, gl, G, 0.f, g);
 #pragma unroll
     for (int i = 0; i < N; ++i) g[i] = f * (float)__float_as_int(g[i]);
-    for (int b = t; b < r.end; b += groups) {
-      const int64_t mine = (int64_t)b + sub;
-      const bool in = mine < r.end;
-      float z[N];
-      load_lane<N, VEC>(A.logits + mine * A.E, in && r.s >= 0, A.E, gl, G, -INFINITY, z);
-      const bool live = in && r.s >= 0 && (!A.mask || A.mask[mine]);
-      if (A.bias) {
-        float bias[N];
-        load_lane<N, VEC>(A.bias, true, A.E, gl, G, 0.f, bias);
-#pragma unroll
-        for (int i = 0; i < N; ++i) z[i] += bias[i];
-      }
-      Token<N, SIGMOID> k;
-      k.set(z, G);
+  };
+  int start = t0;
+  Run r = off.run(A, t0, t1);
+  weights(r.s);
+  for (int b = t0; b < t1; b += groups) {
+    const int mine = b + sub;
+    const bool live = tile.live;
+    tile.add_bias(A, gl);
+    Token<N, SIGMOID> k;
+    k.set(tile.z, G);
+    tile.ask(A, (int64_t)mine + groups, t1, gl);
+    for (;;) {
       float dot = 0.f;
+      if (r.s >= 0) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) dot = fmaf(g[i], k.p[i], dot);
-      dot = group_add(dot, G);
-      const float dl = d1 * k.lse;
-      if (!in || (add && !live)) continue;
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        if constexpr (SIGMOID) z[i] = fmaf(k.p[i] * k.slope[i], g[i] - dot, dl * k.soft[i]);
-        else z[i] = k.p[i] * (g[i] - dot + dl);
-        if (!live) z[i] = 0.f;
+        for (int i = 0; i < N; ++i) dot = fmaf(g[i], k.p[i], dot);
       }
-      float* row = dlogits + mine * A.E;
-      if constexpr (VEC) {
-#pragma unroll
-        for (int i = 0; i < N; i += 4) {
-          const int e = expert<N, VEC>(i, gl, G);
-          if (e >= A.E) break;
-          float4 v = make_float4(z[i], z[i + 1], z[i + 2], z[i + 3]);
-          if (add) {
-            const float4 o = *(const float4*)(row + e);
-            v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
-          }
-          *(float4*)(row + e) = v;
-        }
-      } else {
+      dot = group_add(dot, G);
+      const bool takes = live && r.s >= 0;
+      if (mine >= start && mine < r.end && (takes || !add)) {
+        const float dl = d1 * k.lse;
+        float v[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-          const int e = expert<N, VEC>(i, gl, G);
-          if (e < A.E) row[e] = add ? row[e] + z[i] : z[i];
+          if constexpr (SIGMOID) v[i] = fmaf(k.p[i] * k.slope[i], g[i] - dot, dl * k.soft[i]);
+          else v[i] = k.p[i] * (g[i] - dot + dl);
+          if (!takes) v[i] = 0.f;
+        }
+        float* row = dlogits + (int64_t)mine * A.E;
+        if constexpr (VEC) {
+#pragma unroll
+          for (int i = 0; i < N; i += 4) {
+            const int e = expert<N, VEC>(i, gl, G);
+            if (e >= A.E) break;
+            float4 q = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+            if (add) {
+              const float4 o = *(const float4*)(row + e);
+              q.x += o.x; q.y += o.y; q.z += o.z; q.w += o.w;
+            }
+            *(float4*)(row + e) = q;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            const int e = expert<N, VEC>(i, gl, G);
+            if (e < A.E) row[e] = add ? row[e] + v[i] : v[i];
+          }
         }
       }
+      if (r.end >= t1 || r.end - groups > b) break;  // the chunk ends, or the run goes on behind the tile
+      start = r.end;
+      r = off.run(A, start, t1);
+      weights(r.s);
     }
-    t = r.end;
   }
 }
 
@@ -461,8 +526,8 @@ static Args args_of(const moe_balance_t& c, const float* logits, int ctas, int t
   A.S = c.offsets ? c.S : 1;
   A.group = group_of(c.E);
   A.sigmoid = c.mode == MOE_ROUTE_SIGMOID_GROUPED;
-  // every thread's group has a token where there are enough
-  A.per_chunk = std::max(threads / A.group, ceil_div(c.T, ctas));
+  // few tokens: 16 at least, for few partial sums, where a CTA takes as many at once
+  A.per_chunk = std::max(std::min(threads / A.group, 16), ceil_div(c.T, ctas));
   return A;
 }
 static Args forward_args(const moe_balance_t& c, const float* logits) {
@@ -485,7 +550,7 @@ static Layout layout(const moe_balance_t& c) {
   l.c = take(slots * A.E * 4);
   l.n = take(slots * 4);
   l.z = take(slots * 4);
-  l.loss = take((size_t)A.S * ceil_div(A.E, 32) * 4);
+  l.loss = take((size_t)A.S * ceil_div(A.E, 8) * 4);
   l.zs = take((size_t)A.S * 4);
   l.arrived = take(4);
   l.total = at;
@@ -524,9 +589,9 @@ moe_status_t launch_balance(const moe_balance_t& c, const float* logits, const i
   };
   const moe_status_t st = BALANCE_PICK(partial_kernel, pieces(A, nullptr, nullptr));
   if (st != MOE_OK) return st;
-  const int blocks = A.S * ceil_div(c.E, 32);
-  if (blocks <= 2 * num_sms())
-    return launch_k(sequence_kernel<32>, dim3(blocks), dim3(1024), 0, s, (const Args&)A, (const Sums&)B);
+  const int blocks = A.S * ceil_div(c.E, 8);
+  if (ceil_div(c.T, A.per_chunk) / A.S >= 32)  // slots of a sequence, about
+    return launch_k(sequence_kernel<16>, dim3(blocks), dim3(512), 0, s, (const Args&)A, (const Sums&)B);
   return launch_k(sequence_kernel<4>, dim3(blocks), dim3(128), 0, s, (const Args&)A, (const Sums&)B);
 }
 
