@@ -370,8 +370,7 @@ static moe_status_t backward(const moe_block_t& c, const BlockNormArgs& a, cudaS
     st = BNORM_PICK(backward_kernel, false, MOE_GATE_NONE, false);
   }
   if (st != MOE_OK || blocks == 1) return st;
-  return launch_k(column_sum_kernel, dim3(ceil_div(kinds * c.H, 32)), dim3(1024), 0, s,
-                  (const float*)a.ws, blocks, kinds, c.H, outs);
+  return launch_column_sum(a.ws, blocks, kinds, c.H, outs, s);
 }
 
 }  // namespace bnorm

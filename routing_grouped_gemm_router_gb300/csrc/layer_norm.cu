@@ -381,8 +381,7 @@ static moe_status_t backward(const moe_layer_t& c, const LayerArgs& a, cudaStrea
     return go(backward_kernel<T, I::vpt, I::threads, 1, JOIN, DROP>);
   });
   if (st != MOE_OK || blocks == 1) return st;
-  return launch_k(column_sum_kernel, dim3(ceil_div(kinds * c.H, 32)), dim3(1024), 0, s,
-                  (const float*)a.ws, blocks, kinds, c.H, outs);
+  return launch_column_sum(a.ws, blocks, kinds, c.H, outs, s);
 }
 
 }  // namespace lnorm
