@@ -261,48 +261,39 @@ __device__ __forceinline__ void leave_columns(const Shape& S, uint8_t* smem, int
   }
 }
 
-// Column sums of the partial rows: part[rows][kinds][H] -> out[kind][H]. A block takes 128 columns in
-// pieces of four; warp w adds rows w, w + 32, ... and w + 16, w + 48, ..., then the 32 sums of a column are
-// added in a fixed tree. (With single columns, 32 a block and 32 warps: 6.4 us for 152 rows of 14336, now 4.)
-static __global__ void __launch_bounds__(512) column_sum_kernel(const float* __restrict__ part, int rows,
+// Column sums of the partial rows: part[rows][kinds][H] -> out[kind][H]. A block takes 32 columns in pieces
+// of four: eight threads a row, 32 rows at once; thread group w adds rows w, w + 32, ..., then the 32 sums
+// of a column are added in a fixed tree. Small blocks: the rows' way from L2 bounds it.
+static __global__ void __launch_bounds__(256) column_sum_kernel(const float* __restrict__ part, int rows,
                                                                 int kinds, int H, const Outs out) {
   pdl_wait();
   pdl_trigger();
-  __shared__ float4 sh[32][33];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __shared__ float4 sh[32][9];
   const int64_t width = (int64_t)kinds * H;
-  const int64_t col = (int64_t)blockIdx.x * 128 + lane * 4;
-  float4 s[2] = {make_float4(0, 0, 0, 0), make_float4(0, 0, 0, 0)};
+  const int64_t col = (int64_t)blockIdx.x * 32 + (threadIdx.x & 7) * 4;
+  float4 s = make_float4(0, 0, 0, 0);
   if (col < width) {
-#pragma unroll 4
-    for (int r = warp; r < rows; r += 32) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        if (r + 16 * i >= rows) break;
-        const float4 v = *(const float4*)(part + (r + 16 * i) * width + col);
-        s[i].x += v.x; s[i].y += v.y; s[i].z += v.z; s[i].w += v.w;
-      }
+#pragma unroll 8
+    for (int r = threadIdx.x >> 3; r < rows; r += 32) {
+      const float4 v = *(const float4*)(part + r * width + col);
+      s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
     }
   }
-  sh[warp][lane] = s[0];
-  sh[warp + 16][lane] = s[1];
+  sh[threadIdx.x >> 3][threadIdx.x & 7] = s;
   __syncthreads();
-  // four threads a column, 8 sums each: pairs 16 apart, then 8, 4, 2 and 1
-  const int c = threadIdx.x >> 2, q = threadIdx.x & 3;
-  const float* mine = (const float*)&sh[0][0] + c;
-  constexpr int ROW = 33 * 4;
-  float v[4];
+  // eight threads a column, 4 sums each: pairs 16 apart, then 8, 4, 2 and 1
+  const int c = threadIdx.x >> 3, q = threadIdx.x & 7;
+  const float* mine = (const float*)&sh[q][0] + c;
+  constexpr int STEP = 8 * 9 * 4;
+  float sum = (mine[0] + mine[2 * STEP]) + (mine[STEP] + mine[3 * STEP]);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = mine[(q + 4 * i) * ROW] + mine[(q + 4 * i + 16) * ROW];
-  float sum = (v[0] + v[2]) + (v[1] + v[3]);
-  sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-  sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-  const int64_t to = (int64_t)blockIdx.x * 128 + c;
+  for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  const int64_t to = (int64_t)blockIdx.x * 32 + c;
   if (q == 0 && to < width) out.p[to / H][to % H] = sum;
 }
 inline moe_status_t launch_column_sum(const float* part, int rows, int kinds, int H, const Outs& outs,
                                       cudaStream_t s) {
-  return launch_k(column_sum_kernel, dim3((unsigned)ceil_div64((int64_t)kinds * H, 128)), dim3(512), 0, s, part,
+  return launch_k(column_sum_kernel, dim3((unsigned)ceil_div64((int64_t)kinds * H, 32)), dim3(256), 0, s, part,
                   rows, kinds, H, outs);
 }
 
