@@ -149,17 +149,52 @@ __global__ void __launch_bounds__(512) forward_kernel(const __grid_constant__ Ro
 }
 
 // ------------------------------------------------------------------- backward
+// Sums of N values (2 or 4) over a row's group, in every thread of it, as group_sum: but a warp's lanes
+// divide the values among them, so that 4 values take 6 rounds of shuffles and not 20, and as many again
+// over the warps.
+template <int N>
+__device__ __forceinline__ void divided_sum(float (&v)[N], int group, Reducer& red, int& turn) {
+  constexpr int LANES = 32 / N;  // that hold one value in the end
+  const int lane = threadIdx.x & 31, which = lane / LANES;
+#pragma unroll
+  for (int off = 16, n = N / 2; n > 0; off >>= 1, n >>= 1) {
+    const bool upper = lane & off;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float keep = upper ? v[i + n] : v[i], send = upper ? v[i] : v[i + n];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, off);
+    }
+  }
+  float s = v[0];
+#pragma unroll
+  for (int off = LANES / 2; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+  if (group > 32) {
+    const int warp = threadIdx.x >> 5, w = group >> 5, first = warp / w * w, j = lane % LANES;
+    auto& buf = red.buf[turn];
+    turn ^= 1;
+    if (j == 0) buf[which][warp] = s;
+    __syncthreads();
+    s = j < w ? buf[which][first + j] : 0.f;
+    if (LANES < 16 && j + LANES < w) s += buf[which][first + j + LANES];
+#pragma unroll
+    for (int off = LANES / 2; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xffffffffu, s, i * LANES);
+}
+
 // JOIN: dy too. Row tensors: dh, x, (dres). A group takes ROWS rows at a time, whose sums meet at one barrier
 // and whose weights are loaded once; dh and x stay in registers as they are stored, dres is read from
-// the ring when the sums are there.
-template <typename T, int VPT, int THREADS, int ROWS, bool JOIN, bool DROP>
+// the ring when the sums are there. FLAT (see Ring): no branch between a unit's rows and chunks, whose
+// instructions then interleave.
+template <typename T, int VPT, int THREADS, int ROWS, bool FLAT, bool JOIN, bool DROP>
 __global__ void __launch_bounds__(THREADS, VPT <= 2 && THREADS <= 256 ? 2 : 1)
     backward_kernel(const __grid_constant__ Shape S, const __grid_constant__ LayerArgs A, int kinds,
                     const Outs outs) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Reducer red;
   const int local = threadIdx.x / S.group, g = threadIdx.x - local * S.group;
-  Ring<T, VPT, 3, ROWS> ring(S, smem, local, g);
+  Ring<T, VPT, 3, ROWS, FLAT> ring(S, smem, local, g);
   pdl_wait();
   pdl_trigger();
   ring.start();
@@ -187,8 +222,11 @@ __global__ void __launch_bounds__(THREADS, VPT <= 2 && THREADS <= 256 ? 2 : 1)
   scalars(blockIdx.x);
   F2 w[VPT][4];
 #pragma unroll
-  for (int v = 0; v < VPT; ++v)
+  for (int v = 0; v < VPT; ++v) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[v][i] = zero;
     if (ring.has[v]) load_w(A.gamma, (g + v * S.group) * 8, w[v]);
+  }
   for (int u = blockIdx.x; u < S.units; u += gridDim.x) {
     const int t0 = (u * S.per + local) * ROWS;
     F2 rr[ROWS], mm[ROWS];
@@ -207,11 +245,11 @@ __global__ void __launch_bounds__(THREADS, VPT <= 2 && THREADS <= 256 ? 2 : 1)
     for (int r = 0; r < ROWS; ++r) s1[r] = s2[r] = zero;
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
-      if (!ring.has[v]) continue;
+      if (!FLAT && !ring.has[v]) continue;
       const F2(&ga)[4] = w[v];
 #pragma unroll
       for (int r = 0; r < ROWS; ++r) {
-        if (t0 + r >= S.T) continue;
+        if (!FLAT && t0 + r >= S.T) continue;
         ring.get(dq[r][v], 0, v, t0 + r, r);
         ring.get(xq[r][v], 1, v, t0 + r, r);
         F2 x[4], d[4];
@@ -234,16 +272,16 @@ __global__ void __launch_bounds__(THREADS, VPT <= 2 && THREADS <= 256 ? 2 : 1)
       s[2 * r] = both(s1[r]);
       s[2 * r + 1] = both(s2[r]);
     }
-    group_sum<2 * ROWS>(s, S.group, red, turn);
+    divided_sum<2 * ROWS>(s, S.group, red, turn);
     // dx = dres + r (a - mean(a) - mean(a xn) xn)
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
       const int c = g + v * S.group;
-      if (!ring.has[v]) continue;
+      if (!FLAT && !ring.has[v]) continue;
       const F2(&ga)[4] = w[v];
 #pragma unroll
       for (int r = 0; r < ROWS; ++r) {
-        if (t0 + r >= S.T) continue;
+        if (!FLAT && t0 + r >= S.T) continue;
         const F2 m1 = dup(-s[2 * r] * S.inv_h), m0 = dup(-s[2 * r + 1] * S.inv_h);
         const int64_t at = (int64_t)(t0 + r) * S.H + c * 8;
         F2 x[4], d[4];
@@ -265,12 +303,13 @@ __global__ void __launch_bounds__(THREADS, VPT <= 2 && THREADS <= 256 ? 2 : 1)
 #pragma unroll
           for (int i = 0; i < 4; ++i) d[i] = d[i] * rr[r];
         }
+        const bool live = !FLAT || (t0 + r < S.T && ring.has[v]);
         o.set(d);
-        o.store(A.dx, at);
+        if (live) o.store(A.dx, at);
         if (JOIN) {
           drop_scale<DROP>(d, &rng, A.drop, at);
           o.set(d);
-          o.store(A.dy, at);
+          if (live) o.store(A.dy, at);
         }
       }
     }
@@ -308,9 +347,12 @@ static Shape shape_of(const moe_layer_t& c, int vec, int rows) {
   s.inv_h = 1.0f / (float)c.H;
   return s;
 }
-// Rows that a group takes at a time in the backward kernels: two of bf16, where that leaves every SM work.
-static int rows_of(const moe_layer_t& c) {
-  if (c.dtype != MOE_BF16 || c.H > 8192) return 1;
+// Rows that a group takes at a time in the backward kernels: two of bf16 for the norm alone, where that
+// leaves every SM work; with the join's second gradient and its random numbers registers are better spent
+// on one row without branches (8192 x 4096 69 and 75 us, 8192 x 7168 119 and 128; the norm alone of 7168
+// 81 with one row and 77 with two).
+static int rows_of(const moe_layer_t& c, bool join) {
+  if (join || c.dtype != MOE_BF16 || c.H > 8192) return 1;
   return shape_of(c, wide(c), 2).units >= 2 * num_sms() ? 2 : 1;
 }
 
@@ -322,16 +364,18 @@ struct Instance {
   using T = T_;
   static constexpr int vpt = VPT, threads = THREADS;
 };
-template <typename T, typename F>
-static moe_status_t pick(int vec, int group, F f) {
-  if (vec == 1) return f(Instance<T, 1, 256>{});
-  if (vec == 2) return group <= 256 ? f(Instance<T, 2, 256>{}) : group <= 448 ? f(Instance<T, 2, 448>{}) : f(Instance<T, 2, 512>{});
-  if (vec == 4) return group <= 256 ? f(Instance<T, 4, 256>{}) : f(Instance<T, 4, 512>{});
-  return group <= 256 ? f(Instance<T, 8, 256>{}) : f(Instance<T, 8, 512>{});
-}
 template <typename F>
-static moe_status_t pick(const moe_layer_t& c, int vec, int group, F f) {
-  return c.dtype == MOE_BF16 ? pick<bf>(vec, group, f) : pick<float>(vec, group, f);
+static moe_status_t pick(const moe_layer_t& c, int group, F f) {
+  const int v = wide(c);
+  if (c.dtype == MOE_BF16) {
+    if (v == 1) return f(Instance<bf, 1, 256>{});
+    if (v == 2)
+      return group <= 256 ? f(Instance<bf, 2, 256>{}) : group <= 448 ? f(Instance<bf, 2, 448>{}) : f(Instance<bf, 2, 512>{});
+    return v == 4 ? f(Instance<bf, 4, 512>{}) : f(Instance<bf, 8, 512>{});
+  }
+  if (v == 1) return f(Instance<float, 1, 256>{});
+  if (v == 2) return group <= 256 ? f(Instance<float, 2, 256>{}) : f(Instance<float, 2, 448>{});
+  return v == 4 ? f(Instance<float, 4, 512>{}) : f(Instance<float, 8, 512>{});
 }
 
 template <bool JOIN, bool DROP>
@@ -342,15 +386,19 @@ static moe_status_t forward(const moe_layer_t& c, const LayerArgs& a, cudaStream
   auto go = [&](auto kern) {
     return launch_k(kern, dim3(ceil_div(c.T, per)), dim3(R.warps * 32 * per), 0, s, (const Rows&)R, a);
   };
+  auto with = [&](auto i) {
+    using I = decltype(i);
+    return go(forward_kernel<typename I::T, I::vpt, JOIN, DROP>);
+  };
   if (c.dtype == MOE_BF16)
-    return v == 1   ? go(forward_kernel<bf, 1, JOIN, DROP>)
-           : v == 2 ? go(forward_kernel<bf, 2, JOIN, DROP>)
-           : v == 4 ? go(forward_kernel<bf, 4, JOIN, DROP>)
-                    : go(forward_kernel<bf, 8, JOIN, DROP>);
-  return v == 1   ? go(forward_kernel<float, 1, JOIN, DROP>)
-         : v == 2 ? go(forward_kernel<float, 2, JOIN, DROP>)
-         : v == 4 ? go(forward_kernel<float, 4, JOIN, DROP>)
-                  : go(forward_kernel<float, 8, JOIN, DROP>);
+    return v == 1   ? with(Instance<bf, 1, 512>{})
+           : v == 2 ? with(Instance<bf, 2, 512>{})
+           : v == 4 ? with(Instance<bf, 4, 512>{})
+                    : with(Instance<bf, 8, 512>{});
+  return v == 1   ? with(Instance<float, 1, 512>{})
+         : v == 2 ? with(Instance<float, 2, 512>{})
+         : v == 4 ? with(Instance<float, 4, 512>{})
+                  : with(Instance<float, 8, 512>{});
 }
 
 // Bytes of rows in flight an SM in the backward kernels: with two rows a group, two stages of two CTAs.
@@ -358,7 +406,7 @@ constexpr size_t kBackBudget = 200 * 1024;
 
 template <bool JOIN, bool DROP>
 static moe_status_t backward(const moe_layer_t& c, const LayerArgs& a, cudaStream_t s) {
-  Shape S = shape_of(c, wide(c), rows_of(c));
+  Shape S = shape_of(c, wide(c), rows_of(c, JOIN));
   S.in[S.n_in++] = a.dh;
   S.in[S.n_in++] = a.x;
   if (a.dres) S.in[S.n_in++] = a.dres;
@@ -369,16 +417,20 @@ static moe_status_t backward(const moe_layer_t& c, const LayerArgs& a, cudaStrea
   // the CTA's groups meet in shared memory at the end
   const size_t least = S.per > 1 ? (size_t)S.per * S.H * sizeof(float) : 0;
   int blocks = 0;
-  const moe_status_t st = pick(c, wide(c), S.group, [&](auto i) {
+  const moe_status_t st = pick(c, S.group, [&](auto i) {
     using I = decltype(i);
     using T = typename I::T;
     auto go = [&](auto kern) {
       return run_within(kBackBudget, kern, S, sizeof(T), least, kRinged<T, I::vpt>, kMaxCtas, blocks, s, a, kinds,
                         outs);
     };
-    if constexpr (sizeof(T) == 2 && I::vpt <= 2)
-      if (S.rows == 2) return go(backward_kernel<T, I::vpt, I::threads, 2, JOIN, DROP>);
-    return go(backward_kernel<T, I::vpt, I::threads, 1, JOIN, DROP>);
+    if constexpr (I::vpt <= 2) {
+      if constexpr (sizeof(T) == 2 && !JOIN)  // two rows of two chunks without branches: too many registers
+        if (S.rows == 2) return go(backward_kernel<T, I::vpt, I::threads, 2, I::vpt == 1, JOIN, DROP>);
+      return go(backward_kernel<T, I::vpt, I::threads, 1, true, JOIN, DROP>);
+    } else {
+      return go(backward_kernel<T, I::vpt, I::threads, 1, false, JOIN, DROP>);
+    }
   });
   if (st != MOE_OK || blocks == 1) return st;
   return launch_column_sum(a.ws, blocks, kinds, c.H, outs, s);
@@ -389,7 +441,10 @@ static moe_status_t backward(const moe_layer_t& c, const LayerArgs& a, cudaStrea
 using namespace lnorm;
 
 size_t layer_ws_bytes(const moe_layer_t& c) {
-  return (size_t)rows::max_blocks(shape_of(c, wide(c), rows_of(c))) * 2 * c.H * sizeof(float);
+  // the same size for both kinds of call
+  const int blocks = std::max(rows::max_blocks(shape_of(c, wide(c), rows_of(c, false))),
+                              rows::max_blocks(shape_of(c, wide(c), rows_of(c, true))));
+  return (size_t)blocks * 2 * c.H * sizeof(float);
 }
 
 moe_status_t launch_layer_norm(const moe_layer_t& c, const LayerArgs& a, cudaStream_t s) {

@@ -45,6 +45,7 @@ struct Chunk<__nv_bfloat16> {
   static constexpr int kBytes = 16;
   __device__ __forceinline__ void load(const uint8_t* p) { q = __ldcs((const uint4*)p); }
   __device__ __forceinline__ void load_shared(const uint8_t* p) { q = *(const uint4*)p; }
+  __device__ __forceinline__ void zero() { q = make_uint4(0, 0, 0, 0); }
   __device__ __forceinline__ void get(F2 (&f)[4]) const {
     const uint32_t u[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
@@ -77,6 +78,10 @@ struct Chunk<float> {
   }
   __device__ __forceinline__ void load_shared(const uint8_t* p) {
     set(*(const float4*)p, *((const float4*)p + 1));
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = f2(0.f, 0.f);
   }
   __device__ __forceinline__ void get(F2 (&f)[4]) const {
 #pragma unroll
@@ -138,14 +143,17 @@ __device__ __forceinline__ void group_sum(float (&v)[M], int group, Reducer& red
 
 // A thread's pieces of its next rows. A stage holds, tensor by tensor, the CTA's rows; a thread
 // writes and reads only its own chunks, so the order of its own copies is all that counts. Rows
-// too long for the ring (kRinged) are read from global memory as they are used.
+// too long for the ring (kRinged) are read from global memory as they are used. FLAT: rows behind the last
+// are zeros, and so is what a thread reads of a chunk that it does not hold, so that a row's arithmetic
+// takes no branches.
 template <typename T, int VPT>
 constexpr bool kRinged = VPT * (int)sizeof(T) <= 8;
 
-template <typename T, int VPT, int MAXIN, int ROWS = 1>
+template <typename T, int VPT, int MAXIN, int ROWS = 1, bool FLAT = false>
 struct Ring {
   static constexpr bool on = kRinged<T, VPT>;
   const Shape& S;
+  const uint8_t* base;
   const uint8_t* mine;    // this thread's first chunk in the current stage
   uint32_t first;         // and in stage 0, as a shared address
   uint32_t tensor_bytes, stage_bytes, step;  // step: from a thread's chunk to its next
@@ -153,7 +161,8 @@ struct Ring {
   bool has[VPT];
   int local, stage = 0;
   __device__ __forceinline__ Ring(const Shape& S_, uint8_t* smem, int local_, int g)
-      : S(S_), local(local_) {
+      : S(S_), base(smem), local(local_) {
+    static_assert(on || !FLAT, "zeros come through the ring");
     row_bytes = (uint32_t)S.H * sizeof(T);
     tensor_bytes = row_bytes * S.per * ROWS;
     stage_bytes = tensor_bytes * S.n_in;
@@ -168,8 +177,13 @@ struct Ring {
     if constexpr (on) {
 #pragma unroll
       for (int r = 0; r < ROWS; ++r) {
-        const int t = (u * S.per + local) * ROWS + r;
-        if (u >= S.units || t >= S.T) break;
+        int t = (u * S.per + local) * ROWS + r;
+        if (u >= S.units || (!FLAT && t >= S.T)) break;
+        uint32_t bytes = 16;
+        if (FLAT && t >= S.T) {
+          t = 0;
+          bytes = 0;
+        }
         const int64_t from = (int64_t)t * row_bytes + off;
         uint32_t dst = first + s * stage_bytes + r * row_bytes;
 #pragma unroll
@@ -181,7 +195,7 @@ struct Ring {
             if (has[v]) {
 #pragma unroll
               for (int b = 0; b < Chunk<T>::kBytes; b += 16)
-                cp_async16(dst + v * step + b, src + v * step + b, 16);
+                cp_async16(dst + v * step + b, src + v * step + b, bytes);
             }
           }
           dst += tensor_bytes;
@@ -201,6 +215,11 @@ struct Ring {
   }
   // chunk v of tensor i in row r of the group's rows in the current unit; t: that row
   __device__ __forceinline__ void get(Chunk<T>& q, int i, int v, int t, int r = 0) const {
+    if (FLAT && v == VPT - 1) {  // only a row's last round of chunks has threads without one
+      q.load_shared(has[v] ? mine + i * tensor_bytes + r * row_bytes + v * step : base);
+      if (!has[v]) q.zero();
+      return;
+    }
     if (on) q.load_shared(mine + i * tensor_bytes + r * row_bytes + v * step);
     else q.load((const uint8_t*)S.in[i] + (int64_t)t * row_bytes + off + v * step);
   }
