@@ -73,6 +73,12 @@ Tensor workspace(const moe_layer_t& c, const Tensor& x, size_t& bytes) {
   return empty({(int64_t)bytes}, ScalarType::Byte, x);
 }
 
+// The gradients of a norm's weight and, if it has one, its bias.
+std::array<Tensor, 2> weight_grads(const Tensor& gamma, bool beta) {
+  if (!beta) return {empty_as(gamma), Tensor()};
+  return empties({{{gamma.size(0)}, kF32}, {{gamma.size(0)}, kF32}}, gamma);
+}
+
 OPERATOR(layer_norm) {  // x, gamma, beta or None, eps -> h, mean, rstd
   return guarded(n, 4, [&]() -> PyObject* {
     const Tensor& x = check("x", a[0], {-1, -1}, kAnyFloat, -1);
@@ -80,7 +86,8 @@ OPERATOR(layer_norm) {  // x, gamma, beta or None, eps -> h, mean, rstd
     const Tensor& gamma = check("gamma", a[1], {x.size(1)}, kF32, dev);
     const Tensor beta = given(a[2]) ? check("beta", a[2], {x.size(1)}, kF32, dev) : Tensor();
     const moe_layer_t c = layer(x, 1.f, number(a[3]));
-    const Tensor h = empty_as(x), mean = empty({x.size(0)}, kF32, x), r = empty({x.size(0)}, kF32, x);
+    const Tensor h = empty_as(x);
+    const auto [mean, r] = empties({{{x.size(0)}, kF32}, {{x.size(0)}, kF32}}, x);
     done("moe_layer_norm", moe_layer_norm(&c, ptr(x), fptr(gamma), fmaybe(beta), ptr(h), fptr(mean), fptr(r),
                                           stream_of(x)));
     return tuple({h, mean, r});
@@ -99,8 +106,8 @@ OPERATOR(layer_norm_backward) {  // dh, x, gamma, mean, rstd, dres or None, beta
     const Tensor dres = given(a[5]) ? check("dres", a[5], {T, H}, x.scalar_type(), dev) : Tensor();
     const moe_layer_t c = layer(x, 1.f, 0.f);
     size_t bytes = 0;
-    const Tensor ws = workspace(c, x, bytes), dx = empty_as(x), dg = empty_as(gamma);
-    const Tensor db = truth(a[6]) ? empty_as(gamma) : Tensor();
+    const Tensor ws = workspace(c, x, bytes), dx = empty_as(x);
+    const auto [dg, db] = weight_grads(gamma, truth(a[6]));
     done("moe_layer_norm_backward",
          moe_layer_norm_backward(&c, ptr(dh), ptr(x), fptr(gamma), fptr(mean), fptr(r), maybe(dres), ptr(dx),
                                  fptr(dg), fmaybe(db), ptr(ws), bytes, stream_of(x)));
@@ -133,8 +140,9 @@ OPERATOR(dropout_join) {
       gn = check("gamma_next", a[6], {H}, kF32, dev);
       if (given(a[7])) bn = check("beta_next", a[7], {H}, kF32, dev);
       h = empty_as(x);
-      mean = empty({T}, kF32, x);
-      r = empty({T}, kF32, x);
+      auto stats = empties({{{T}, kF32}, {{T}, kF32}}, x);
+      mean = std::move(stats[0]);
+      r = std::move(stats[1]);
     } else if (given(a[7])) {
       throw Refused{"beta_next: needs gamma_next"};
     }
@@ -172,8 +180,8 @@ OPERATOR(dropout_join_backward) {
     const moe_drop_t d = drop_of(a[1], a[2], a[3], dev);
     const moe_layer_t c = layer(out, number(a[4]), 0.f);
     size_t bytes = 0;
-    const Tensor ws = workspace(c, out, bytes), dx = empty_as(out), dy = empty_as(out), dg = empty_as(gn);
-    const Tensor db = truth(a[10]) ? empty_as(gn) : Tensor();
+    const Tensor ws = workspace(c, out, bytes), dx = empty_as(out), dy = empty_as(out);
+    const auto [dg, db] = weight_grads(gn, truth(a[10]));
     done("moe_dropout_join_backward",
          moe_dropout_join_backward(&c, &d, maybe(dres), ptr(dh), ptr(out), fptr(gn), fptr(mean), fptr(r), ptr(dx),
                                    ptr(dy), fptr(dg), fmaybe(db), ptr(ws), bytes, stream_of(out)));
@@ -216,9 +224,8 @@ OPERATOR(balance_loss) {
     size_t bytes = 0;
     done("moe_balance_workspace_size", moe_balance_workspace_size(&c, &bytes));
     const Tensor ws = empty({(int64_t)bytes}, ScalarType::Byte, logits);
-    const Tensor losses = empty({2}, kF32, logits), totals = empty({2}, kI32, logits);
-    const Tensor counts = empty({c.S, c.E}, kI32, logits), tokens = empty({c.S}, kI32, logits);
-    const Tensor prob = empty({c.S, c.E}, kF32, logits);
+    const auto [losses, counts, tokens, prob, totals] =
+        empties({{{2}, kF32}, {{c.S, c.E}, kI32}, {{c.S}, kI32}, {{c.S, c.E}, kF32}, {{2}, kI32}}, logits);
     done("moe_balance_loss",
          moe_balance_loss(&c, fptr(logits), iptr(ids), fptr(losses), iptr(counts), iptr(tokens), fptr(prob),
                           iptr(totals), ptr(ws), bytes, stream_of(logits)));
