@@ -582,6 +582,12 @@ size_t embed_ws_bytes(int T, int V, int H) { return layout(T, H).total; }
 moe_status_t launch_embed_backward(const void* dx, const void* tokens, bool wide, int T, int V, int H,
                                    moe_dtype_t dt, moe_dtype_t out_dt, float scale, int accumulate,
                                    void* dtable, void* ws, cudaStream_t s) {
+  const int vec = (int)((size_t)H * dtype_size(dt) / 16), slices = ceil_div(vec, 32);
+  const int chunks = ceil_div(T, kRun);
+  const int64_t blocks = ceil_div64((int64_t)chunks * slices, 8);
+  const int columns = ceil_div(H, 128);
+  const int64_t joins = (int64_t)ceil_div(chunks, 8) * columns;
+  if (blocks > 0x7fffffff || joins > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
   const Layout l = layout(T, H);
   uint8_t* w = (uint8_t*)ws;
   SortArgs A{};
@@ -603,12 +609,6 @@ moe_status_t launch_embed_backward(const void* dx, const void* tokens, bool wide
   const uint32_t* keys = A.key[0];
   const int32_t* at = A.at[0];
   float* part = (float*)(w + l.part);
-  const int vec = (int)((size_t)H * dtype_size(dt) / 16), slices = ceil_div(vec, 32);
-  const int chunks = ceil_div(T, kRun);
-  const int64_t blocks = ceil_div64((int64_t)chunks * slices, 8);
-  const int columns = ceil_div(H, 128);
-  const int64_t joins = (int64_t)ceil_div(chunks, 8) * columns;
-  if (blocks > 0x7fffffff || joins > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
   const bool add = accumulate != 0;
   auto sums = [&](auto run, auto join, auto* out) {
     const moe_status_t r = launch_k(run, dim3((unsigned)blocks), dim3(256), 0, s, (const uint4*)dx, keys, at, T,
