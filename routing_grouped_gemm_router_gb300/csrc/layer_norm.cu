@@ -319,9 +319,12 @@ __global__ void __launch_bounds__(THREADS, VPT <= 2 && THREADS <= 256 ? 2 : 1)
   if (kinds > 1) leave_columns<VPT>(S, smem, local, g, sb, 1, kinds, 1.f, A.ws, outs);
 }
 
-// Chunks of 8 elements a thread holds. Backward, two: the sums over tokens take 16 registers a chunk.
-static int wide(const moe_layer_t& c) {
+// Chunks of 8 elements a thread holds. Backward, two: the sums over tokens take 16 registers a chunk. One
+// for the norm alone with a few rows an SM, where a row's latency counts: 600 x 2000 in fp32 12.9 and 10.4 us,
+// 1531 x 2056 17.6 and 15.7 (the join's gradient, longer in a thread, takes as long either way).
+static int wide(const moe_layer_t& c, bool join) {
   const int chunks = c.H / 8;
+  if (!join && chunks <= 512 && c.T >= 2 * num_sms() && c.T <= 16 * num_sms()) return 1;
   const int two = c.dtype == MOE_F32 ? 896 : 1024;
   return chunks <= 32 ? 1 : chunks <= two ? 2 : chunks <= 2048 ? 4 : 8;
 }
@@ -353,7 +356,7 @@ static Shape shape_of(const moe_layer_t& c, int vec, int rows) {
 // 81 with one row and 77 with two).
 static int rows_of(const moe_layer_t& c, bool join) {
   if (join || c.dtype != MOE_BF16 || c.H > 8192) return 1;
-  return shape_of(c, wide(c), 2).units >= 2 * num_sms() ? 2 : 1;
+  return shape_of(c, wide(c, join), 2).units >= 2 * num_sms() ? 2 : 1;
 }
 
 using bf = __nv_bfloat16;
@@ -365,15 +368,14 @@ struct Instance {
   static constexpr int vpt = VPT, threads = THREADS;
 };
 template <typename F>
-static moe_status_t pick(const moe_layer_t& c, int group, F f) {
-  const int v = wide(c);
+static moe_status_t pick(const moe_layer_t& c, int v, int group, F f) {
   if (c.dtype == MOE_BF16) {
-    if (v == 1) return f(Instance<bf, 1, 256>{});
+    if (v == 1) return group <= 256 ? f(Instance<bf, 1, 256>{}) : f(Instance<bf, 1, 512>{});
     if (v == 2)
       return group <= 256 ? f(Instance<bf, 2, 256>{}) : group <= 448 ? f(Instance<bf, 2, 448>{}) : f(Instance<bf, 2, 512>{});
     return v == 4 ? f(Instance<bf, 4, 512>{}) : f(Instance<bf, 8, 512>{});
   }
-  if (v == 1) return f(Instance<float, 1, 256>{});
+  if (v == 1) return group <= 256 ? f(Instance<float, 1, 256>{}) : f(Instance<float, 1, 512>{});
   if (v == 2) return group <= 256 ? f(Instance<float, 2, 256>{}) : f(Instance<float, 2, 448>{});
   return v == 4 ? f(Instance<float, 4, 512>{}) : f(Instance<float, 8, 512>{});
 }
@@ -406,7 +408,7 @@ constexpr size_t kBackBudget = 200 * 1024;
 
 template <bool JOIN, bool DROP>
 static moe_status_t backward(const moe_layer_t& c, const LayerArgs& a, cudaStream_t s) {
-  Shape S = shape_of(c, wide(c), rows_of(c, JOIN));
+  Shape S = shape_of(c, wide(c, JOIN), rows_of(c, JOIN));
   S.in[S.n_in++] = a.dh;
   S.in[S.n_in++] = a.x;
   if (a.dres) S.in[S.n_in++] = a.dres;
@@ -417,7 +419,7 @@ static moe_status_t backward(const moe_layer_t& c, const LayerArgs& a, cudaStrea
   // the CTA's groups meet in shared memory at the end
   const size_t least = S.per > 1 ? (size_t)S.per * S.H * sizeof(float) : 0;
   int blocks = 0;
-  const moe_status_t st = pick(c, S.group, [&](auto i) {
+  const moe_status_t st = pick(c, wide(c, JOIN), S.group, [&](auto i) {
     using I = decltype(i);
     using T = typename I::T;
     auto go = [&](auto kern) {
@@ -442,8 +444,8 @@ using namespace lnorm;
 
 size_t layer_ws_bytes(const moe_layer_t& c) {
   // the same size for both kinds of call
-  const int blocks = std::max(rows::max_blocks(shape_of(c, wide(c), rows_of(c, false))),
-                              rows::max_blocks(shape_of(c, wide(c), rows_of(c, true))));
+  auto blocks_of = [&](bool join) { return rows::max_blocks(shape_of(c, wide(c, join), rows_of(c, join))); };
+  const int blocks = std::max(blocks_of(false), blocks_of(true));
   return (size_t)blocks * 2 * c.H * sizeof(float);
 }
 
