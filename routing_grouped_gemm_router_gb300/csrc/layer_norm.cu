@@ -74,25 +74,42 @@ __global__ void __launch_bounds__(512) forward_kernel(const __grid_constant__ Ro
     if (JOIN) xq[v].load(from_x + c * Chunk<T>::kBytes);
   }
   Philox rng = DROP ? Philox(A.drop) : Philox();
-  F2 o[VPT][4], s = dup(0.f);
+  // The row stays as it is stored where that takes half the registers: more rows in flight for two more
+  // conversions (norm of 8192 x 4096 32 -> 28.5 us, join without dropout 46 -> 43).
+  constexpr bool PACKED = sizeof(T) == 2;
+  F2 wide[PACKED ? 1 : VPT][4], s = dup(0.f);
+  auto piece = [&](int v, F2 (&o)[4]) {
+    if constexpr (PACKED) {
+      q[v].get(o);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = wide[v][i];
+    }
+  };
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
     const int c = g + v * group;
     if (c >= R.chunks) break;
-    q[v].get(o[v]);
+    F2 o[4];
+    q[v].get(o);
     if (JOIN) {
-      drop_scale<DROP>(o[v], &rng, A.drop, row + c * 8);
+      drop_scale<DROP>(o, &rng, A.drop, row + c * 8);
       F2 x[4];
       xq[v].get(x);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) o[v][i] = o[v][i] + x[i];
+      for (int i = 0; i < 4; ++i) o[i] = o[i] + x[i];
       Chunk<T> out;
-      out.set(o[v]);
+      out.set(o);
       out.store(A.out, row + c * 8);
-      out.get(o[v]);  // the norm reads what is stored
+      out.get(o);  // the norm reads what is stored
+      if constexpr (PACKED) q[v] = out;
+    }
+    if constexpr (!PACKED) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) wide[v][i] = o[i];
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s = s + o[v][i];
+    for (int i = 0; i < 4; ++i) s = s + o[i];
   }
   if (JOIN && !A.gamma) return;
   // a warp's own mean, and the sum of squares about it
@@ -104,9 +121,11 @@ __global__ void __launch_bounds__(512) forward_kernel(const __grid_constant__ Ro
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
     if (g + v * group >= R.chunks) break;
+    F2 o[4];
+    piece(v, o);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const F2 d = o[v][i] + near;
+      const F2 d = o[i] + near;
       s = fma2(d, d, s);
     }
   }
@@ -134,12 +153,13 @@ __global__ void __launch_bounds__(512) forward_kernel(const __grid_constant__ Ro
   for (int v = 0; v < VPT; ++v) {
     const int c = g + v * group;
     if (c >= R.chunks) break;
-    F2 ga[4], be[4];
+    F2 ga[4], be[4], o[4];
+    piece(v, o);
     load_w(A.gamma, c * 8, ga);
     if (A.beta) load_w(A.beta, c * 8, be);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const F2 xn = (o[v][i] + mm) * rr;
+      const F2 xn = (o[i] + mm) * rr;
       ga[i] = A.beta ? fma2(xn, ga[i], be[i]) : xn * ga[i];
     }
     Chunk<T> h;
@@ -328,13 +348,15 @@ static int wide(const moe_layer_t& c, bool join) {
   const int two = c.dtype == MOE_F32 ? 896 : 1024;
   return chunks <= 32 ? 1 : chunks <= two ? 2 : chunks <= 2048 ? 4 : 8;
 }
-// Forward, up to eight (fp32: four), so that few warps share a row's reductions; with few rows for an SM as
-// few as give a row 512 threads at most: one row's latency counts.
-static int narrow(const moe_layer_t& c) {
+// Forward, four, or eight for long rows, so that few warps share a row's reductions (8192 rows of bf16, four and
+// eight, us: norm of 4096 28.5 and 29.4, of 7168 52 and 50; join 56 and 58, 125 and 97; join without dropout
+// 43 and 46, 72 and 75, at every length). With few rows for an SM as few as give a row 512 threads at most:
+// one row's latency counts.
+static int narrow(const moe_layer_t& c, bool join, bool drop) {
   const int chunks = c.H / 8;
   if (c.T < 4 * num_sms()) return chunks <= 32 ? 1 : chunks <= 1024 ? 2 : chunks <= 2048 ? 4 : 8;
-  if (c.dtype == MOE_F32 && chunks <= 2048) return chunks <= 32 ? 1 : chunks <= 64 ? 2 : 4;
-  return chunks <= 32 ? 1 : chunks <= 64 ? 2 : chunks <= 128 ? 4 : 8;
+  const int four = c.dtype == MOE_F32 || (join && !drop) ? 2048 : 640;
+  return chunks <= 32 ? 1 : chunks <= 64 ? 2 : chunks <= four ? 4 : 8;
 }
 static Shape shape_of(const moe_layer_t& c, int vec, int rows) {
   Shape s{};
@@ -382,7 +404,7 @@ static moe_status_t pick(const moe_layer_t& c, int v, int group, F f) {
 
 template <bool JOIN, bool DROP>
 static moe_status_t forward(const moe_layer_t& c, const LayerArgs& a, cudaStream_t s) {
-  const int v = narrow(c);
+  const int v = narrow(c, JOIN, DROP);
   Rows R{c.T, c.H, c.H / 8, ceil_div(c.H / 8, 32 * v), c.eps, 1.0f / (float)c.H};
   const int per = R.warps == 1 ? 4 : 1;
   auto go = [&](auto kern) {
