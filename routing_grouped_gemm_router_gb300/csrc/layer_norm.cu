@@ -53,8 +53,10 @@ struct Rows {
 // asked for at once and stay in registers, and a CTA is done after its row: with many small CTAs an SM has
 // enough rows in flight to hide the chain of a row's reductions. (With persistent CTAs and the
 // rings of the backward kernels three rows an SM were in flight, and 8192 rows of 4096 took 36 us.)
-template <typename T, int VPT, bool JOIN, bool DROP>
-__global__ void __launch_bounds__(512) forward_kernel(const __grid_constant__ Rows R,
+// THREADS, CTAS: of a CTA at most, and at least an SM where that is not 0. The join of bf16 rows in four chunks a
+// thread is held to 72 registers: 8192 x 4096 54 us, with 93 as the compiler likes it 56.
+template <typename T, int VPT, int THREADS, int CTAS, bool JOIN, bool DROP>
+__global__ void __launch_bounds__(THREADS, CTAS) forward_kernel(const __grid_constant__ Rows R,
                                                       const __grid_constant__ LayerArgs A) {
   __shared__ float near_mean[16], near_m2[16];
   const int group = R.warps * 32, local = threadIdx.x / group, g = threadIdx.x - local * group;
@@ -349,7 +351,7 @@ static int wide(const moe_layer_t& c, bool join) {
   return chunks <= 32 ? 1 : chunks <= two ? 2 : chunks <= 2048 ? 4 : 8;
 }
 // Forward, four, or eight for long rows, so that few warps share a row's reductions (8192 rows of bf16, four and
-// eight, us: norm of 4096 28.5 and 29.4, of 7168 52 and 50; join 56 and 58, 125 and 97; join without dropout
+// eight, us: norm of 4096 28.5 and 29.4, of 7168 52 and 50; join 54 and 58, 105 and 97; join without dropout
 // 43 and 46, 72 and 75, at every length). With few rows for an SM as few as give a row 512 threads at most:
 // one row's latency counts.
 static int narrow(const moe_layer_t& c, bool join, bool drop) {
@@ -412,7 +414,10 @@ static moe_status_t forward(const moe_layer_t& c, const LayerArgs& a, cudaStream
   };
   auto with = [&](auto i) {
     using I = decltype(i);
-    return go(forward_kernel<typename I::T, I::vpt, JOIN, DROP>);
+    using T = typename I::T;
+    if constexpr (JOIN && DROP && sizeof(T) == 2 && I::vpt == 4)
+      if (R.warps * 32 * per <= 160) return go(forward_kernel<T, 4, 160, 5, JOIN, DROP>);
+    return go(forward_kernel<T, I::vpt, 512, 0, JOIN, DROP>);
   };
   if (c.dtype == MOE_BF16)
     return v == 1   ? with(Instance<bf, 1, 512>{})
