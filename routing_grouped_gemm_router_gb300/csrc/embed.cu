@@ -11,6 +11,8 @@
 //              lies inside; a run that crosses to other warps' rows leaves fp32 partial sums
 //   join       the partial sums of a run are added in order: a run of any length is spread over as many
 //              warps as it has rows / 16
+// 8192 tokens into 32000 x 4096 in fp32 (591 MB) 75 us of zeros, 26 of sums, 7 of joins; added to a gradient
+// that is there, 44 (174 MB) with 9 of sorting.
 #include "stack.cuh"
 #include "tc_ptx.cuh"
 #include "train.cuh"
@@ -32,7 +34,7 @@ __device__ __forceinline__ int id_of(const void* tokens, int64_t t, int V) {  //
 
 // ------------------------------------------------------------------- lookup
 // A warp takes P pieces a lane of a token's row at a time. Few tokens: one piece a lane, to spread
-// over more warps.
+// over more warps. 16384 tokens of 7168 channels in bf16 52 us: 94 MB of rows read, 235 MB written, 6.3 TB/s.
 template <typename T, bool WIDE, int P>
 __global__ void __launch_bounds__(256) embed_kernel(const void* __restrict__ tokens, int n,
                                                     const uint4* __restrict__ table, int V, int vec,
