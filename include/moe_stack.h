@@ -93,7 +93,8 @@ moe_status_t moe_layer_norm_backward(const moe_layer_t* cfg, const void* dh, con
 
 /* out = x + scale * dropout(y), and with gamma_next the layer norm before the next block in the
  * same pass: h, mean, rstd of out as it is stored. gamma_next, h, mean and rstd are all given or
- * all NULL; beta_next may be NULL. out may be x or y. */
+ * all NULL; beta_next may be NULL. out may be x or y. What is kept is rounded to fp32 as moe_dropout
+ * stores it in fp32, then x is added. */
 moe_status_t moe_dropout_join(const moe_layer_t* cfg, const moe_drop_t* drop, const void* x,
                               const void* y, const float* gamma_next, const float* beta_next,
                               void* out, void* h, float* mean, float* rstd, cudaStream_t stream);
