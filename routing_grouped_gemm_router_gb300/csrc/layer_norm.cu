@@ -238,15 +238,17 @@ __global__ void __launch_bounds__(THREADS, VPT <= 2 && THREADS <= 256 ? 2 : 1)
 #pragma unroll
     for (int i = 0; i < 4; ++i) sg[v][i] = sb[v][i] = zero;
 
-  // a row's scalars are asked for one unit ahead: nothing else hides their way from L2
+  // a row's scalars are asked for one unit ahead: nothing else hides their way from L2. FLAT: 0 for rows behind
+  // the last and threads that hold no chunk, whose xn has to be 0 and not (0 - mean) * rstd of some row.
   float m_next[ROWS], r_next[ROWS];
   auto scalars = [&](int64_t u) {
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
       int64_t t = (u * S.per + local) * ROWS + r;
+      const bool some = !FLAT || (t < S.T && (VPT > 1 || ring.has[0]));
       if (t >= S.T) t = 0;
-      m_next[r] = __ldg(A.mean_in + t);
-      r_next[r] = __ldg(A.rstd_in + t);
+      m_next[r] = some ? __ldg(A.mean_in + t) : 0.f;
+      r_next[r] = some ? __ldg(A.rstd_in + t) : 0.f;
     }
   };
   scalars(blockIdx.x);
@@ -281,7 +283,7 @@ __global__ void __launch_bounds__(THREADS, VPT <= 2 && THREADS <= 256 ? 2 : 1)
       for (int r = 0; r < ROWS; ++r) {
         if (!FLAT && t0 + r >= S.T) continue;
         ring.get(dq[r][v], 0, v, t0 + r, r);
-        ring.get(xq[r][v], 1, v, t0 + r, r);
+        ring.template get<VPT == 1>(xq[r][v], 1, v, t0 + r, r);  // two chunks a thread: every one has its first
         F2 x[4], d[4];
         dq[r][v].get(d);
         xq[r][v].get(x);

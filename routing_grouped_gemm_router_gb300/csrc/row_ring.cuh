@@ -144,7 +144,7 @@ __device__ __forceinline__ void group_sum(float (&v)[M], int group, Reducer& red
 // A thread's pieces of its next rows. A stage holds, tensor by tensor, the CTA's rows; a thread
 // writes and reads only its own chunks, so the order of its own copies is all that counts. Rows
 // too long for the ring (kRinged) are read from global memory as they are used. FLAT: rows behind the last
-// are zeros, and so is what a thread reads of a chunk that it does not hold, so that a row's arithmetic
+// are zeros, and a thread reads something of a chunk that it does not hold (see get), so that a row's arithmetic
 // takes no branches.
 template <typename T, int VPT>
 constexpr bool kRinged = VPT * (int)sizeof(T) <= 8;
@@ -213,11 +213,15 @@ struct Ring {
     else if (S.stages == 2) cp_async_wait<1>();
     else cp_async_wait<2>();
   }
-  // chunk v of tensor i in row r of the group's rows in the current unit; t: that row
+  // chunk v of tensor i in row r of the group's rows in the current unit; t: that row. ZEROS: where the thread does
+  // not hold the chunk, zeros, otherwise its first chunk of the row, whose values the row's mean and
+  // deviation fit: (0 - mean) * rstd can be infinite where no element's value is.
+  template <bool ZEROS = true>
   __device__ __forceinline__ void get(Chunk<T>& q, int i, int v, int t, int r = 0) const {
     if (FLAT && v == VPT - 1) {  // only a row's last round of chunks has threads without one
-      q.load_shared(has[v] ? mine + i * tensor_bytes + r * row_bytes + v * step : base);
-      if (!has[v]) q.zero();
+      const uint8_t* row = mine + i * tensor_bytes + r * row_bytes;
+      q.load_shared(has[v] ? row + v * step : ZEROS ? base : row);
+      if (ZEROS && !has[v]) q.zero();
       return;
     }
     if (on) q.load_shared(mine + i * tensor_bytes + r * row_bytes + v * step);

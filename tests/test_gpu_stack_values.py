@@ -1,9 +1,10 @@
 """The operators around a stack's blocks at values that their formulas allow and few inputs hold. Tolerances as
 in test_gpu_stack."""
+import numpy as np
 import pytest
 import torch
 
-from test_gpu_stack import BF, DEV, F32, gen, randn
+from test_gpu_stack import BF, DEV, F32, F64, U, check_norm_grad, gen, norm_grad_ref, randn, within, words
 
 pytestmark = pytest.mark.gpu
 
@@ -23,6 +24,34 @@ def L():
 def M(L):
     from routing_grouped_gemm_router_gb300 import training
     return training
+
+
+# Row lengths that fill the last round of a row's chunks and ones that do not; rows that fill the last unit of
+# rows and ones that do not.
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T,H", [(1, 8), (3, 72), (37, 264), (1531, 264), (700, 2056), (9, 4096), (701, 4104), (1301, 7168),
+                                 (2, 8200)])
+def test_gradient_of_rows_of_one_huge_value(M, T, H, dtype):
+    """x - mean is 0 in such a row, and so is all that is multiplied by it, though mean * rstd is over the
+    largest number (2^120 * 2^10)."""
+    g = gen(T + H)
+    x, dh, dres = randn(g, T, H, dtype=dtype), randn(g, T, H, dtype=dtype), randn(g, T, H, dtype=dtype)
+    gamma, beta = 1 + randn(g, H, std=0.3), randn(g, H)
+    eps = 2.0 ** -20
+    n = M.layer_norm(x, gamma, beta, eps)
+    huge = torch.arange(T, device=DEV) % 3 == 0  # the first row among them
+    x[huge] = 2.0 ** 120
+    n.mean[huge] = 2.0 ** 120
+    n.rstd[huge] = 2.0 ** 10
+    for res in (dres, None):
+        got = M.layer_norm_backward(dh, x, gamma, n.mean, n.rstd, dres=res)
+        check_norm_grad(got.dx, got.dgamma, got.dbeta, dh, x, gamma, n.mean, n.rstd, res, True)
+        rng = torch.tensor([3, 4], device=DEV)
+        b = M.dropout_join_backward(res, 0.25, rng, 1, 1.0, dh, x, gamma, n.mean, n.rstd)
+        check_norm_grad(b.dx, b.dgamma_next, b.dbeta_next, dh, x, gamma, n.mean, n.rstd, res, True)
+        f = torch.from_numpy((words(T * H, 3, 4, 1) >= np.uint64(1 << 30)).reshape(T, H)).to(DEV).to(F64) / 0.75
+        dx, off, _ = norm_grad_ref(dh, x, gamma, n.mean, n.rstd, res)
+        within(b.dy, f * dx, f * (off + 3 * U * dx.abs()), "dy")
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
