@@ -49,8 +49,8 @@ class TokenBlockSaved(NamedTuple):
 
 
 class TokenStackSaved(NamedTuple):
-    tokens: torch.Tensor
-    rng: torch.Tensor  # as it was in the forward pass
+    tokens: torch.Tensor  # these, rng, offsets and mask: as they were in the forward pass
+    rng: torch.Tensor
     x: torch.Tensor
     mean: torch.Tensor
     rstd: torch.Tensor
@@ -103,7 +103,8 @@ class TokenStack:
 
     def forward(self, tokens, offsets=None, mask=None):
         """(h[T, H], losses[blocks, 2], saved) for token ids [T], int32 or int64. offsets and mask: the packed
-        sequences and the tokens that take part in the router's losses (``balance_loss``)."""
+        sequences and the tokens that take part in the router's losses (``balance_loss``). The caller's
+        tensors may be written once the call has returned."""
         rng = self.rng.clone()  # the backward pass draws the same numbers, whatever is written meanwhile
         x = ops.embed(tokens, self.table, self.embed_scale)
         if self.p:
@@ -119,7 +120,9 @@ class TokenStack:
             out, h = j.out, j.h
             saved.append(TokenBlockSaved(s, bal, out, j.mean, j.rstd))
         losses = torch.stack([s.balance.losses for s in saved])
-        return h, losses, TokenStackSaved(tokens, rng, x, mean, rstd, saved, offsets, mask)
+        # copies: a program may fill its buffers with the next batch before the backward pass
+        inputs = [None if t is None else t.clone() for t in (tokens, offsets, mask)]
+        return h, losses, TokenStackSaved(inputs[0], rng, x, mean, rstd, saved, *inputs[1:])
 
     __call__ = forward
 
