@@ -57,11 +57,13 @@ class TokenStackSaved(NamedTuple):
     blocks: List[TokenBlockSaved]
     offsets: Optional[torch.Tensor]
     mask: Optional[torch.Tensor]
+    p: float  # of the forward pass's dropout
 
 
 class TokenStack:
     """table[V, H] in the blocks' type; gamma_final[H], and beta_final[H] or None, fp32; p: dropout after the
-    embedding and in every join; seed: of the random numbers."""
+    embedding and in every join (set to 0 for a pass without; a backward pass takes its forward pass's); seed: of
+    the random numbers."""
 
     def __init__(self, table, blocks: List[TokenBlock], gamma_final, beta_final=None, embed_scale: float = 1.0,
                  p: float = 0.0, seed: int = 0, eps: float = 1e-5):
@@ -122,7 +124,7 @@ class TokenStack:
         losses = torch.stack([s.balance.losses for s in saved])
         # copies: a program may fill its buffers with the next batch before the backward pass
         inputs = [None if t is None else t.clone() for t in (tokens, offsets, mask)]
-        return h, losses, TokenStackSaved(inputs[0], rng, x, mean, rstd, saved, *inputs[1:])
+        return h, losses, TokenStackSaved(inputs[0], rng, x, mean, rstd, saved, *inputs[1:], self.p)
 
     __call__ = forward
 
@@ -133,7 +135,7 @@ class TokenStack:
         for i in reversed(range(len(self.blocks))):
             b, s = self.blocks[i], saved.blocks[i]
             gamma, beta, grads, gname, bname = self._norm_after(i)
-            j = ops.dropout_join_backward(dres, self.p, saved.rng, 1 + i, b.scale, dh, s.out, gamma, s.mean,
+            j = ops.dropout_join_backward(dres, saved.p, saved.rng, 1 + i, b.scale, dh, s.out, gamma, s.mean,
                                           s.rstd, beta is not None)
             grads[gname].add_(j.dgamma_next)
             if beta is not None:
@@ -145,6 +147,6 @@ class TokenStack:
         g["gamma"].add_(n.dgamma)
         if first.beta is not None:
             g["beta"].add_(n.dbeta)
-        dx = ops.dropout(n.dx, self.p, saved.rng, 0) if self.p else n.dx
+        dx = ops.dropout(n.dx, saved.p, saved.rng, 0) if saved.p else n.dx
         ops.embed_backward(dx, saved.tokens, self.table.shape[0], self.embed_scale, out=self.grads["table"],
                            accumulate=True)

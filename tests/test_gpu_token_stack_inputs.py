@@ -32,3 +32,25 @@ def test_inputs_may_be_written_before_the_backward_pass(S):
     want = grads(lambda: None)
     got = grads(next_batch)
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_a_pass_without_dropout_between_forward_and_backward(S):
+    """A validation pass with p set to 0 in between leaves the gradients as they are."""
+    T = 40
+    stack, rnd = make(S, torch.float32, p=0.3)
+    tokens, dh = tokens_of(T, 5), rnd(T, H)
+
+    def grads(between):
+        stack.p = 0.3
+        stack.zero_grad()
+        saved = stack.forward(tokens)[2]
+        between()
+        stack.backward(dh, saved)
+        return [t.clone() for g in (stack.grads, *stack.block_grads) for t in g.values()]
+
+    def validate():
+        stack.p = 0.0
+        stack.forward(tokens_of(T, 6))
+
+    want = grads(lambda: None)
+    assert all(torch.equal(a, b) for a, b in zip(grads(validate), want))
