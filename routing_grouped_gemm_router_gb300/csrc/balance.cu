@@ -126,7 +126,7 @@ struct Token {
 #pragma unroll
     for (int i = 0; i < N; ++i) m = fmaxf(m, z[i]);
     m = group_max(m, group);
-    // exponentials of base 2: off by 2 steps, and half a step for every unit of the arguments' size
+    // exponentials of base 2: off by 2 steps, and by half a step for every unit of z - m
     constexpr float kLog2e = 1.4426950408889634f;
     const float shift = -m * kLog2e;
     float sum = 0.f, total = 0.f;
@@ -138,7 +138,11 @@ struct Token {
     if constexpr (SIGMOID) {
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const float x = exp2_fast(-fabsf(z[i]) * kLog2e), d = reciprocal_fast(1.f + x);
+        // an accurate exponential: a rounded product of z and log2(e) alone puts x off by up to 16 half steps at
+        // z = -20, 58 at -60 (above, the error is that of the difference to the largest, which any form has).
+        // The reciprocal is off by one step whatever z. Both directions, 8191 tokens of 256 experts, 23.2 us with the
+        // approximate exponential, 24.1 so, 26.3 with a true division too.
+        const float x = expf(-fabsf(z[i])), d = reciprocal_fast(1.f + x);
         soft[i] = p[i];
         p[i] = m < 0.f ? p[i] * d : z[i] >= 0.f ? d : x * d;
         slope[i] = z[i] >= 0.f ? x * d : d;

@@ -66,3 +66,20 @@ def test_the_join_adds_what_dropout_gives(M, T, H, dtype):
         want = (x.float() + M.dropout(y.float(), p, rng, 4, scale)).to(dtype)
         assert torch.equal(M.dropout_join(x, y, p, rng, 4, scale).out, want)
         assert torch.equal(M.dropout_join(x, y, p, rng, 4, scale, gamma).out, want)
+
+
+def test_probabilities_of_sigmoids_far_below_the_largest(M):
+    """A sequence a token: prob is the tokens' probabilities. A sigmoid of z < 0 is x / (1 + x), x = exp(z): off by 2
+    steps (an exponential, whatever its argument), a step for the reciprocal, and half a step for 1 + x and the
+    product: 8 half steps. The sum over experts is off by as much and half a step for each of 16 + 5
+    additions, its reciprocal and the last product by one each: 39."""
+    g = gen(31)
+    T, E, k = 700, 64, 2
+    z = -80 * torch.rand(T, E, generator=g, device=DEV)
+    z[:, ::16] = randn(g, T, 4).abs()
+    ids = z.topk(k, 1).indices.to(torch.int32)
+    offsets = torch.arange(T + 1, dtype=torch.int32, device=DEV)
+    b = M.balance_loss(z, ids, mode=1, offsets=offsets)
+    ref = torch.sigmoid(z.to(F64))
+    ref = ref / ref.sum(1, keepdim=True)
+    assert (b.prob.to(F64) / ref - 1).abs().max() <= 40 * U
