@@ -351,12 +351,28 @@ __global__ void __launch_bounds__(THREADS, VPT <= 2 && THREADS <= 256 ? 2 : 1)
   if (kinds > 1) leave_columns<VPT>(S, smem, local, g, sb, 1, kinds, 1.f, A.ws, outs);
 }
 
-// Chunks of 8 elements a thread holds. Backward, two: the sums over tokens take 16 registers a chunk. One
-// for the norm alone with a few rows an SM, where a row's latency counts: 600 x 2000 in fp32 12.9 and 10.4 us,
-// 1531 x 2056 17.6 and 15.7 (the join's gradient, longer in a thread, takes as long either way).
+// Chunks of 8 elements a thread holds. Backward, two: the sums over tokens take 16 registers a chunk. One for the
+// norm alone where that was quicker; one and two, us in a graph (the join's gradient, longer in a thread,
+// takes as long either way):
+//   rows                 200         400         800        1216        2432        4864   of channels
+//   1000 bf16        6.3  5.9    7.7  6.7    7.5  8.3    7.7  8.0   11.1 11.4   14.9 15.9
+//        fp32        6.4  6.2    8.0  7.2    8.9 10.0   10.6 10.9   14.4 14.7   20.9 19.6
+//   2056 bf16        7.2  7.2    6.7  9.5    9.6 11.3   11.4 12.8   16.2 17.3   25.9 22.6
+//        fp32        8.0  8.0    8.5 11.4   12.0 14.8   14.0 17.1   20.7 22.3   34.4 37.7
+//   4096 bf16        7.7  9.0    9.5 10.3   13.5 13.7   15.4 15.7   21.6 20.7   33.7 32.5
+//        fp32        9.5 11.2   12.9 13.4   17.7 17.9   21.7 19.8   34.5 32.3   58.8 56.9
+// Two CTAs fit an SM. In two chunks a thread, rows of 129 to 288 chunks give them 3 to 6 warps each, in one 5 to
+// 9. Shorter rows fill a CTA either way, several at once: one chunk a thread halves the rows of a CTA, which helps
+// once every SM has some. Longer ones leave one CTA an SM: only while that one has few rows.
+static bool one_chunk(const moe_layer_t& c) {
+  const int chunks = c.H / 8, sms = num_sms();
+  if (chunks <= 128) return c.T >= 8 * sms && c.T <= 16 * sms;
+  if (chunks <= 288) return c.T <= 16 * sms;
+  return chunks <= 512 && c.T > sms && c.T <= 3 * sms;
+}
 static int wide(const moe_layer_t& c, bool join) {
   const int chunks = c.H / 8;
-  if (!join && chunks <= 512 && c.T >= 2 * num_sms() && c.T <= 16 * num_sms()) return 1;
+  if (!join && one_chunk(c)) return 1;
   const int two = c.dtype == MOE_F32 ? 896 : 1024;
   return chunks <= 32 ? 1 : chunks <= two ? 2 : chunks <= 2048 ? 4 : 8;
 }
