@@ -83,3 +83,21 @@ def test_probabilities_of_sigmoids_far_below_the_largest(M):
     ref = torch.sigmoid(z.to(F64))
     ref = ref / ref.sum(1, keepdim=True)
     assert (b.prob.to(F64) / ref - 1).abs().max() <= 40 * U
+
+
+def test_dropout_on_both_sides_of_the_2_34th_element(M, L):
+    """From there on the upper word of the generator's counter is not 0. In place, through the C entry point."""
+    H = 32768
+    T = (1 << 34) // H + 3
+    if torch.cuda.mem_get_info()[0] < 3 * T * H:
+        pytest.skip("not enough free memory")
+    x = torch.ones(T, H, dtype=BF, device=DEV)
+    rng = torch.tensor([2 ** 62 + 77, 2 ** 35 + 1], device=DEV)
+    cfg = L.moe_layer_t(T=T, H=H, dtype=L.MOE_BF16, scale=1.0)
+    L.moe_dropout(cfg, L.moe_drop_t(p=0.5, rng=rng.data_ptr(), site=9), x, x)
+    start = (T - 6) * H
+    want = torch.from_numpy(words(6 * H, 2 ** 62 + 77, 2 ** 35 + 1, 9, start) >= np.uint64(1 << 31)).view(6, H)
+    assert start < 1 << 34 < T * H
+    assert torch.equal(x[-6:].cpu(), 2.0 * want.to(BF))
+    del x
+    torch.cuda.empty_cache()
