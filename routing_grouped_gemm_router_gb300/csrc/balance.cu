@@ -12,8 +12,9 @@
 // place of its own for every pair of a chunk and a sequence that meet, since both only grow along the
 // tokens. A second kernel adds a sequence's slots in order. Counts are integers, everything else is
 // added in a fixed order.
-// Measured, from a cold L2: 32768 tokens of 128 experts 9 us, 7 for the second kernel, 8 backward (16, 8 and 20
-// with a warp a token; the bytes need 2.5 each way); 8191 of 256 in 13 sequences 9, 6 and 8.
+// Measured, from a cold L2: 32768 tokens of 128 experts, softmax, 9 us, 7 for the second kernel, 9 backward (16, 8
+// and 20 with a warp a token; the bytes need 2.5 each way); 8191 of 256, sigmoids, in 13 sequences 10, 6 and 9.
+// With the logits in L2 22 and 24 us in all; added to a gradient that is there 10 and 5 more.
 #include "stack.cuh"
 #include "train.cuh"
 

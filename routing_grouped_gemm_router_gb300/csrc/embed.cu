@@ -267,7 +267,7 @@ __device__ __forceinline__ void sort_any(const SortArgs& A, SortShared& sh) {
 }
 
 // Zeros into the rows of ids that do not occur: the CTA marks the ids of its rows that do, and every
-// thread has the others' rows written by bulk copies from a buffer of zeros (7 TB/s; with a warp's
+// thread has the others' rows written by bulk copies from a buffer of zeros (6.3 TB/s; with a warp's
 // stores row by row 4.1).
 template <bool WIDE>
 __device__ __forceinline__ void fill_zeros(const SortArgs& A, FillShared& sh, int cta, int ctas) {

@@ -7,11 +7,12 @@
 //   back   a = dh gamma:  d = dres + r (a - mean(a) - xn mean(a xn));  dx = d,  dy = scale keep d
 //          dgamma = sum_t dh xn;  dbeta = sum_t dh
 // Every row is read once and written once, so HBM bounds all of them, but where random numbers are drawn: the
-// mask is computed from the element's number wherever it is needed, which takes as many instructions as
-// the rest. The backward kernels' rows go through the rings and the column sums of row_ring.cuh.
-// Measured, 8192 rows of bf16, us and TB/s: norm of 4096 channels 28 (4.7), of 7168 50 (4.7); its gradient with a
-// residual 49 (5.5), 76 (6.2); join with the next norm 43 (6.2), 72 (6.5), with dropout 54 (5.0), 97 (4.9);
-// its gradient with dropout 69 (4.9), 118 (5.0); dropout alone 27 (5.0), 46 (5.1).
+// mask is computed from the element's number wherever it is needed, which takes a third of a join's
+// instructions (116 of 336 for eight elements). The backward kernels' rows go through the rings and the column sums of row_ring.cuh.
+// Measured, 8192 rows of bf16, us and TB/s: norm of 4096 channels 28.5 (4.7), of 7168 50 (4.7); its gradient with a
+// residual 49 (5.5), 76.5 (6.1); join with the next norm 43.5 (6.2), 73 (6.5), with dropout 55 (4.9), 98 (4.8);
+// its gradient with dropout 68 (4.9), 118.5 (5.0); dropout alone 27 (5.0), 46 (5.1). Of fp32, 4096 channels: 47 (5.7),
+// 90 (5.9), 82 (6.5), 86 (6.2), 120.5 (5.6), 42 (6.4).
 //
 // The variance is summed about a mean that is already near the row's: a warp sums its own elements,
 // then their squared distances from its own mean, and the warps' sums and distances are joined by
@@ -62,7 +63,7 @@ struct Rows {
 // enough rows in flight to hide the chain of a row's reductions. (With persistent CTAs and the
 // rings of the backward kernels three rows an SM were in flight, and 8192 rows of 4096 took 36 us.)
 // THREADS, CTAS: of a CTA at most, and at least an SM where that is not 0. The join of bf16 rows in four chunks a
-// thread is held to 72 registers: 8192 x 4096 54 us, with 93 as the compiler likes it 56.
+// thread is held to 72 registers: 8192 x 4096 55 us, with 92 as the compiler likes it 56.5.
 template <typename T, int VPT, int THREADS, int CTAS, bool JOIN, bool DROP>
 __global__ void __launch_bounds__(THREADS, CTAS)
     forward_kernel(const __grid_constant__ Rows R, const __grid_constant__ LayerArgs A) {
@@ -353,7 +354,7 @@ __global__ void __launch_bounds__(THREADS, VPT <= 2 && THREADS <= 256 ? 2 : 1)
 
 // Chunks of 8 elements a thread holds. Backward, two: the sums over tokens take 16 registers a chunk. One for the
 // norm alone where that was quicker; one and two, us in a graph (the join's gradient, longer in a thread,
-// takes as long either way):
+// loses: 8192 x 4096 76 and 69):
 //   rows                 200         400         800        1216        2432        4864   of channels
 //   1000 bf16        6.3  5.9    7.7  6.7    7.5  8.3    7.7  8.0   11.1 11.4   14.9 15.9
 //        fp32        6.4  6.2    8.0  7.2    8.9 10.0   10.6 10.9   14.4 14.7   20.9 19.6
@@ -377,8 +378,8 @@ static int wide(const moe_layer_t& c, bool join) {
   return chunks <= 32 ? 1 : chunks <= two ? 2 : chunks <= 2048 ? 4 : 8;
 }
 // Forward, four, or eight for long rows, so that few warps share a row's reductions (8192 rows of bf16, four and
-// eight, us: norm of 4096 28.5 and 29.4, of 7168 52 and 50; join 54 and 58, 105 and 97; join without dropout
-// 43 and 46, 72 and 75, at every length). With few rows for an SM as few as give a row 512 threads at most:
+// eight, us: norm of 4096 28.5 and 29.5, of 7168 51.5 and 49.5; join 55 and 58, 126 and 97; join without dropout
+// 43 and 46, 72 and 76, at every length). With few rows for an SM as few as give a row 512 threads at most:
 // one row's latency counts.
 static int narrow(const moe_layer_t& c, bool join, bool drop) {
   const int chunks = c.H / 8;
@@ -402,7 +403,7 @@ static Shape shape_of(const moe_layer_t& c, int vec, int rows) {
 }
 // Rows that a group takes at a time in the backward kernels: two of bf16 for the norm alone, where that
 // leaves every SM work; with the join's second gradient and its random numbers registers are better spent
-// on one row without branches (8192 x 4096 69 and 75 us, 8192 x 7168 119 and 128; the norm alone of 7168
+// on one row without branches (8192 x 4096 69 and 75 us, 8192 x 7168 118 and 128; the norm alone of 7168
 // 81 with one row and 77 with two).
 static int rows_of(const moe_layer_t& c, bool join) {
   if (join || c.dtype != MOE_BF16 || c.H > 8192) return 1;

@@ -23,7 +23,7 @@ struct Drop {
 // Here c = (b, b >> 32, stream, stream >> 32): all that does not depend on the low word of b is computed
 // once (one product of the first round, one of the second), the round keys are kept in registers.
 // A round is then two products and two exclusive-ors of three; with the keys' sums and all products in
-// every round a join issued 369 instructions for eight elements and not 335. A product keeps the
+// every round a join issued 34 instructions more for eight elements (336 now). A product keeps the
 // multiplier pipe four cycles: 36 for eight elements are 144 of the 350 cycles that HBM leaves for a
 // warp's eight elements a lane in a join of bf16 rows.
 struct Philox {

@@ -206,7 +206,7 @@ class SparseStack:
                 t.zero_()
 
     def forward(self, x):
-        """(out[T, H], saved) for x[T, H]."""
+        """(out[T, H], saved) for x[T, H], which saved holds by reference: it stays as it is until ``backward``."""
         first = self.blocks[0]
         first._check_tokens("x", x)
         h, rstd = ops.block_norm(x, first.gamma_in, first.eps)
