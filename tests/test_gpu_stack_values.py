@@ -101,3 +101,17 @@ def test_dropout_on_both_sides_of_the_2_34th_element(M, L):
     assert torch.equal(x[-6:].cpu(), 2.0 * want.to(BF))
     del x
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T,H", [(1215, 1024), (1217, 1024), (2433, 1024), (3, 1032), (700, 1032), (2433, 1032), (307, 2304),
+                                 (152, 2312), (153, 2312), (457, 2312), (155, 4096)])
+def test_norm_gradient_around_its_kernels_borders(M, T, H, dtype):
+    """One or two chunks a thread go by the length of a row and the number of rows."""
+    g = gen(T * 3 + H)
+    x, dh, dres = randn(g, T, H, dtype=dtype), randn(g, T, H, dtype=dtype), randn(g, T, H, dtype=dtype)
+    gamma, beta = 1 + randn(g, H, std=0.3), randn(g, H)
+    n = M.layer_norm(x, gamma, beta)
+    got = M.layer_norm_backward(dh, x, gamma, n.mean, n.rstd, dres=dres)
+    check_norm_grad(got.dx, got.dgamma, got.dbeta, dh, x, gamma, n.mean, n.rstd, dres, True)
+    assert all(torch.equal(a, b) for a, b in zip(got, M.layer_norm_backward(dh, x, gamma, n.mean, n.rstd, dres=dres)))
